@@ -25,6 +25,9 @@ Sources (titles of the pages, with the part each function follows):
     (its formulas were lost in extraction; the readings used are listed in the
     module docstrings).
 
+The activations, the epilogue, its backward and the 8-bit activation checkpoint
+(``act.py``) come from their own definitions, stated there.
+
 Parity status: every function is pinned by tests in ``tests/test_oracle_*.py``
 (closed forms, invariants, brute force, library cross-checks); none is
 "parity unpinned".
@@ -53,5 +56,6 @@ from .int4 import (
     int4_levels, int4_levels_f32, int4_midpoints, int4_encode, quantize_int4, dequantize_int4,
     relative_rms_error,
 )
+from .act import ACTS, CK_BLOCK, act, act_slope, ck_quantize, ck_values, act_fwd, act_bwd
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -1,4 +1,5 @@
-"""Thin Python binding over the C ABI of ``libqlora_mi355x.so`` (``include/qlora.h``).
+"""Thin Python binding over the C ABI of ``libqlora_mi355x.so`` (``include/qlora.h``
+and ``include/qlora_act.h``).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels.  torch provides device memory (tensors) and the current stream.  The
@@ -74,6 +75,35 @@ _SIGS["nf4_dequantize_dq_grouped"] = (ctypes.c_int, [ctypes.c_int, ctypes.POINTE
 # fp16 compute type: the same arguments as the bf16 entry point of the same stem
 for _n in ("nf4_quantize_dq", "nf4_dequantize_dq", "qlora_linear_fwd", "qlora_linear_bwd_input", "qlora_merge_lora"):
     _SIGS[_n + "_f16"] = _SIGS[_n]
+
+
+class Epilogue(ctypes.Structure):
+    """qlora_epilogue: what follows the product in qlora_linear_act_fwd."""
+    _fields_ = [("act", ctypes.c_int), ("bias", _c_p), ("mul", _c_p), ("residual", _c_p), ("z", _c_p),
+                ("z_codes", _c_p), ("z_scale", _c_p)]
+
+
+class Saved(ctypes.Structure):
+    """qlora_saved: one saved activation, 16-bit values or a checkpoint."""
+    _fields_ = [("values", _c_p), ("codes", _c_p), ("scale", _c_p)]
+
+
+class ActGrad(ctypes.Structure):
+    """qlora_act_grad: saved activations and outputs of qlora_linear_act_bwd."""
+    _fields_ = [("act", ctypes.c_int), ("x", Saved), ("z", Saved), ("mul", Saved), ("dx_add", _c_p), ("dx", _c_p),
+                ("d_lora_a", _c_p), ("d_lora_b", _c_p), ("d_bias", _c_p), ("d_mul", _c_p)]
+
+
+_SIGS["act8_quantize"] = (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p])
+_SIGS["act8_dequantize"] = (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p])
+_fwd_tail = [_c_p, _c_p, _c_i64, ctypes.c_float, ctypes.POINTER(Epilogue), _c_p, _c_p, ctypes.c_size_t, _c_p]
+_bwd_tail = [_c_p, _c_p, _c_i64, ctypes.c_float, ctypes.POINTER(ActGrad), _c_p, ctypes.c_size_t, _c_p]
+for _n, _tail in (("qlora_linear_act_fwd", _fwd_tail), ("qlora_linear_act_bwd", _bwd_tail)):
+    _SIGS[_n] = (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p] + _tail)
+    _SIGS[_n + "_sq"] = (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p] + _tail)
+for _n in ("act8_quantize", "act8_dequantize", "qlora_linear_act_fwd", "qlora_linear_act_bwd"):
+    _SIGS[_n + "_f16"] = _SIGS[_n]
+_SIGS["qlora_act_workspace_bytes_bwd"] = (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64])
 EXPORTS = tuple(_SIGS)
 
 REUSE_FORWARD = 1   # QLORA_BWD_REUSE_FORWARD
@@ -551,6 +581,223 @@ def qlora_merge_lora(qw, lora_a=None, lora_b=None, scaling=1.0, out=None, dtype=
     _check(fn, getattr(lib(), fn)(
         _ptr(qw.codes), *sc, qw.K, qw.N, _ptr(lora_a), _ptr(lora_b), r, float(scaling), _ptr(out), _stream()))
     return out
+
+
+# ------------------------------------------------------------------ epilogue forward, 8-bit checkpoints, their backward
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}    # QLORA_ACT_*
+
+
+def _act(name):
+    if name not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, not {name!r}")
+    return ACTS[name]
+
+
+@dataclass
+class Act8:
+    """8-bit checkpoint of an activation (device tensors): one code per value, one scale per 64."""
+    codes: torch.Tensor       # int8 [numel]
+    scale: torch.Tensor       # float32 [ceil(numel/64)]
+    shape: tuple              # of the activation
+
+    @property
+    def numel(self):
+        n = 1
+        for d in self.shape:
+            n *= d
+        return n
+
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.scale.numel()
+
+
+def _check_act8(a8, name):
+    """The checkpoint's tensors must hold exactly what its shape needs."""
+    _shape(a8.codes.reshape(-1), (a8.numel,), f"{name} codes")
+    _shape(a8.scale.reshape(-1), (-(-a8.numel // 64),), f"{name} scale")
+
+
+def act8_empty(shape, device="cuda"):
+    """An Act8 of uninitialised storage for an activation of `shape`."""
+    n = 1
+    for d in shape:
+        n *= d
+    return Act8(torch.empty(n, dtype=torch.int8, device=device),
+                torch.empty(-(-n // 64), dtype=torch.float32, device=device), tuple(shape))
+
+
+def act8_quantize(x, out=None):
+    """bf16 or fp16 activation of any shape -> Act8 (written into `out` if given)."""
+    ct = _ct(x, "x")
+    if out is not None:
+        _check_act8(out, "out")
+        _shape(x, out.shape, "x")
+    _dev(x, x.dtype, "x")
+    if out is None:
+        out = act8_empty(x.shape, x.device)
+    _dev(out.codes, torch.int8, "out codes")
+    _dev(out.scale, torch.float32, "out scale")
+    fn = "act8_quantize" + ct
+    _check(fn, getattr(lib(), fn)(_ptr(x), x.numel(), _ptr(out.codes), _ptr(out.scale), _stream()))
+    return out
+
+
+def act8_dequantize(a8, dtype=torch.bfloat16, out=None):
+    """Act8 -> the 16-bit values it stands for, in `dtype` (or in the dtype of `out`)."""
+    _check_act8(a8, "checkpoint")
+    _shape(out, a8.shape, "out")
+    _dev(a8.codes, torch.int8, "codes")
+    _dev(a8.scale, torch.float32, "scale")
+    if out is None:
+        out = torch.empty(a8.shape, dtype=dtype, device=a8.codes.device)
+    fn = "act8_dequantize" + _ct(out, "out")
+    _dev(out, out.dtype, "out")
+    _check(fn, getattr(lib(), fn)(_ptr(a8.codes), _ptr(a8.scale), a8.numel, _ptr(out), _stream()))
+    return out
+
+
+def qlora_linear_act_fwd(x, qw, lora_a=None, lora_b=None, scaling=1.0, bias=None, act="none", mul=None,
+                         residual=None, save=None, workspace=None, out=None, z=None):
+    """Y = act(Z) * mul + residual with Z = X W'^T + scaling (X A) B + bias; x [T, K] -> y [T, N].
+    `act` is one of ACTS; bias [N], mul and residual [T, N] are left out when None.  `out` may be
+    the tensor of mul or of residual.  save="z" returns (y, Z) with Z in 16 bits, save="z8" (y,
+    Act8 of that Z), for qlora_linear_act_bwd; `z` is the tensor or Act8 to save into."""
+    ct = _ct(x, "x")
+    code = _act(act)
+    if save not in (None, "z", "z8"):
+        raise ValueError(f"save must be None, 'z' or 'z8', not {save!r}")
+    if z is not None and (save is None or isinstance(z, Act8) != (save == "z8")):
+        raise ValueError("z is given with save, a tensor for 'z' and an Act8 for 'z8'")
+    _check_storage(qw)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [T, K], got shape {tuple(x.shape)}")
+    T, N = x.shape[0], qw.N
+    _shape(x, (T, qw.K), "x")
+    r = _check_adapters(lora_a, lora_b, qw.K, N)
+    _shape(bias, (N,), "bias")
+    for t, name in ((mul, "mul"), (residual, "residual"), (out, "out")):
+        _shape(t, (T, N), name)
+    if z is not None:
+        if save == "z8":
+            _check_act8(z, "z")
+        if tuple(z.shape) != (T, N):
+            raise ValueError(f"z has shape {tuple(z.shape)}, expected {(T, N)}")
+    for t, name in ((x, "x"), (lora_a, "lora_a"), (lora_b, "lora_b"), (bias, "bias"), (mul, "mul"),
+                    (residual, "residual"), (out, "out")):
+        _dev(t, x.dtype, name)
+    if out is None:
+        out = torch.empty((T, N), dtype=x.dtype, device=x.device)
+    if save and z is None:
+        z = act8_empty((T, N), x.device) if save == "z8" else torch.empty_like(out)
+    if save == "z8":
+        _dev(z.codes, torch.int8, "z codes")
+        _dev(z.scale, torch.float32, "z scale")
+    elif save:
+        _dev(z, x.dtype, "z")
+    if workspace is None:
+        workspace = workspace_for(T, qw.K, N, r, x.device)
+    ep = Epilogue(code, _ptr(bias), _ptr(mul), _ptr(residual), _ptr(z) if save == "z" else None,
+                  _ptr(z.codes) if save == "z8" else None, _ptr(z.scale) if save == "z8" else None)
+    fn = _entry("qlora_linear_act_fwd", ct, qw)
+    _check(fn, getattr(lib(), fn)(
+        _ptr(x), T, qw.K, N, _ptr(qw.codes), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r, float(scaling),
+        ctypes.byref(ep), _ptr(out), _ptr(workspace), workspace.numel(), _stream()))
+    return (out, z) if save else out
+
+
+@dataclass
+class ActGrads:
+    """Gradients of qlora_linear_act_bwd; None where not asked for."""
+    dx: torch.Tensor
+    d_lora_a: torch.Tensor = None
+    d_lora_b: torch.Tensor = None
+    d_bias: torch.Tensor = None
+    d_mul: torch.Tensor = None
+
+
+def qlora_act_workspace_bytes_bwd(T, K, N, r):
+    return int(lib().qlora_act_workspace_bytes_bwd(T, K, N, r))
+
+
+def _saved(v, shape, dtype, name):
+    """Checks of one saved activation (tensor or Act8) against its shape."""
+    if isinstance(v, Act8):
+        _check_act8(v, name)
+        if tuple(v.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(v.shape)}, expected {tuple(shape)}")
+    else:
+        _shape(v, shape, name)
+
+
+def _saved_arg(v, dtype, name):
+    if isinstance(v, Act8):
+        _dev(v.codes, torch.int8, name + " codes")
+        _dev(v.scale, torch.float32, name + " scale")
+        return Saved(None, v.codes.data_ptr(), v.scale.data_ptr())
+    _dev(v, dtype, name)
+    return Saved(_ptr(v), None, None)
+
+
+def qlora_linear_act_bwd(dy, qw, lora_a=None, lora_b=None, scaling=1.0, act="none", x=None, z=None, mul=None,
+                         lora_grads=False, bias_grad=False, mul_grad=True, dx_add=None, workspace=None, dx=None,
+                         d_lora_a=None, d_lora_b=None, d_bias=None, d_mul=None):
+    """Backward of qlora_linear_act_fwd for upstream gradient dy [T, N] -> ActGrads.  x [T, K], z and
+    mul [T, N] are what the forward had (z: before the activation), each a 16-bit tensor or an
+    Act8.  x is needed for lora_grads, z for an activation or the gradient of mul (computed when
+    mul is given and mul_grad).  dX gets dx_add [T, K] added before its rounding (`dx` may be that
+    tensor)."""
+    ct = _ct(dy, "dy")
+    code = _act(act)
+    _check_storage(qw)
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be 2-D [T, N], got shape {tuple(dy.shape)}")
+    T, N, K = dy.shape[0], qw.N, qw.K
+    _shape(dy, (T, N), "dy")
+    r = _check_adapters(lora_a, lora_b, K, N)
+    mul_grad = mul_grad and mul is not None
+    if lora_grads and r == 0:
+        raise ValueError("lora_grads needs the adapters")
+    if lora_grads and x is None:
+        raise ValueError("lora_grads needs x")
+    if z is None and (code or mul_grad):
+        raise ValueError("an activation or the gradient of mul needs z")
+    _saved(x, (T, K), dy.dtype, "x")
+    _saved(z, (T, N), dy.dtype, "z")
+    _saved(mul, (T, N), dy.dtype, "mul")
+    _shape(dx_add, (T, K), "dx_add")
+    outs = {"dx": (dx, (T, K), True), "d_lora_a": (d_lora_a, (K, r), lora_grads),
+            "d_lora_b": (d_lora_b, (r, N), lora_grads), "d_bias": (d_bias, (N,), bias_grad),
+            "d_mul": (d_mul, (T, N), mul_grad)}
+    for name, (t, shape, asked) in outs.items():
+        if t is not None and not asked:
+            raise ValueError(f"{name} is given but its gradient is not asked for")
+        _shape(t, shape, name)
+    for t, name in ((dy, "dy"), (lora_a, "lora_a"), (lora_b, "lora_b"), (dx_add, "dx_add")):
+        _dev(t, dy.dtype, name)
+    g = ActGrad(act=code, dx_add=_ptr(dx_add))
+    if x is not None:
+        g.x = _saved_arg(x, dy.dtype, "x")
+    if z is not None:
+        g.z = _saved_arg(z, dy.dtype, "z")
+    if mul is not None:
+        g.mul = _saved_arg(mul, dy.dtype, "mul")
+    res = {}
+    for name, (t, shape, asked) in outs.items():
+        if asked:
+            if t is None:
+                t = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+            _dev(t, dy.dtype, name)
+            setattr(g, name, t.data_ptr())
+            res[name] = t
+    if workspace is None:
+        n = qlora_act_workspace_bytes_bwd(T, K, N, r)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dy.device)
+    fn = _entry("qlora_linear_act_bwd", ct, qw)
+    _check(fn, getattr(lib(), fn)(
+        _ptr(dy), T, K, N, _ptr(qw.codes), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r, float(scaling),
+        ctypes.byref(g), _ptr(workspace), workspace.numel(), _stream()))
+    return ActGrads(**res)
 
 
 # The _sq entry points under their C names (the wrappers above pick them for an NF4WeightSQ).

@@ -3,9 +3,12 @@
 // here; every buffer comes from the caller.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 #include "qlora.h"
+#include "qlora_act.h"
+#include "act.hpp"
 #include "common.hpp"
 #include "grad.hpp"
 #include "plan.hpp"
@@ -17,10 +20,11 @@ hipError_t launch_lora_down_x(const uint16_t* x, float scaling, const LoraPlan& 
 hipError_t launch_lora_down_dy(const uint16_t* dy, const uint16_t* lora_b, float scaling, const LoraPlan& pl,
                                uint8_t* ws, bool transposed, hipStream_t s, bool f16, const ScalesJob* scales);
 hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, const uint16_t* lora_b,
-                      const LoraPlan& pl, const uint8_t* ws, uint16_t* y, hipStream_t s, bool f16);
+                      const LoraPlan& pl, const uint8_t* ws, uint16_t* y, hipStream_t s, bool f16,
+                      const Epilogue* epi);
 hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, const uint16_t* lora_a,
                      const LoraPlan& pl, const uint8_t* ws, uint16_t* dx, hipStream_t s, bool f16,
-                     bool scales_ready, const FusedGrads* fused);
+                     bool scales_ready, const FusedGrads* fused, const uint16_t* dx_add);
 hipError_t launch_lora_grads(const uint16_t* x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws,
                              uint16_t* d_lora_a, uint16_t* d_lora_b, hipStream_t s, bool f16);
 FusedGrads fused_grads_for(const uint16_t* x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws, bool da,
@@ -110,9 +114,22 @@ size_t fwd_workspace(int64_t T, int64_t K, int64_t N, int64_t r, size_t cap = SI
     return pl.fwd_bytes;
 }
 
+// The epilogue of the token rows from t0 on.
+ql::Epilogue epilogue_rows(ql::Epilogue e, int64_t t0, int64_t N) {
+    if (e.mul) e.mul += t0 * N;
+    if (e.res) e.res += t0 * N;
+    if (e.z) e.z += t0 * N;
+    if (e.zc) {
+        e.zc += t0 * N;
+        e.zs += t0 * N / 64;
+    }
+    return e;
+}
+
 int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* codes, ql::BlockScales sc,
              const uint16_t* lora_a, const uint16_t* lora_b, int64_t r, float scaling, uint16_t* y, void* workspace,
-             size_t workspace_bytes, void* stream, bool f16 = false, size_t cap = SIZE_MAX) {
+             size_t workspace_bytes, void* stream, bool f16 = false, size_t cap = SIZE_MAX,
+             const ql::Epilogue* epi = nullptr) {
     if (int st = fwd_check(x, T, K, N, codes, sc, lora_a, lora_b, r, scaling, y)) return st;
     if (workspace && !aligned16(workspace)) return QLORA_ERR_ALIGN;
     const ql::LoraPlan pl(T, K, N, r, cap);
@@ -123,7 +140,7 @@ int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (T <= ql::kGemvMaxT)      // decode sizes: small-M MFMA, split-k partials
-        return dev(ql::launch_gemv(x, codes, sc, lora_a, lora_b, scaling, pl, ws, y, s, f16));
+        return dev(ql::launch_gemv(x, codes, sc, lora_a, lora_b, scaling, pl, ws, y, s, f16, epi));
     if (chunked) {
         // small prefill: kGemvMaxT-token windows as the problems of one grouped
         // decode launch pair (they share the weight).  Window c starts at token
@@ -131,12 +148,15 @@ int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
         // predecessor, computes those rows identically and skips writing them.
         const int64_t windows = (T + ql::kGemvMaxT - 1) / ql::kGemvMaxT;
         ql::GemvProblem g[ql::kMaxGroup];
+        ql::Epilogue ge[ql::kMaxGroup];
         for (int64_t c = 0; c < windows; ++c) {
             const int64_t t0 = std::min<int64_t>(c * ql::kGemvMaxT, T - ql::kGemvMaxT);
             g[c] = ql::GemvProblem{x + t0 * K, codes, sc, lora_a, lora_b, scaling, K, N, y + t0 * N,
                                    c * ql::kGemvMaxT - t0};
+            if (epi) ge[c] = epilogue_rows(*epi, t0, N);
         }
-        return dev(ql::launch_gemv_group(g, (int)windows, ql::kGemvMaxT, r, ws, s, f16));
+        return dev(ql::launch_gemv_group(g, (int)windows, ql::kGemvMaxT, r, ws, s, f16, ql::DecodeProduct::Auto,
+                                         epi ? ge : nullptr));
     }
     if (r > 0) {
         if (int st = dev(ql::launch_transpose_a(lora_a, pl, ws, s))) return st;
@@ -144,7 +164,42 @@ int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
         // QLORA_BWD_REUSE_FORWARD take the adapter gradients without recomputing it
         if (int st = dev(ql::launch_lora_down_x(x, scaling, pl, ws, true, s, f16))) return st;
     }
-    return dev(ql::launch_fwd(x, codes, sc, lora_b, pl, ws, y, s, f16));
+    return dev(ql::launch_fwd(x, codes, sc, lora_b, pl, ws, y, s, f16, epi));
+}
+
+// Launch sequence of the backward (arguments checked): dX (plus dx_add if
+// given), and dA, dB where asked for.
+int bwd_launch(const uint16_t* dy, const uint8_t* codes, ql::BlockScales sc, const uint16_t* lora_a,
+               const uint16_t* lora_b, float scaling, uint16_t* dx, const uint16_t* dx_add, const uint16_t* x,
+               uint16_t* d_lora_a, uint16_t* d_lora_b, const ql::LoraPlan& pl, uint8_t* ws, bool reuse, bool fused,
+               hipStream_t s, bool f16) {
+    const int64_t r = pl.r;
+    const bool grads = d_lora_a || d_lora_b;
+    if (r > 0) {
+        // s dY B^T, with the dX kernel's block scales as extra workgroups of the same launch
+        const ql::ScalesJob sj = ql::scales_job_for(sc, pl, ws);
+        if (int st = dev(ql::launch_lora_down_dy(dy, lora_b, scaling, pl, ws, grads, s, f16, &sj))) return st;
+    }
+    // s X A (both layouts) for dB when the forward's is not reused
+    auto recompute_p = [&]() -> int {
+        if (int st = dev(ql::launch_transpose_a(lora_a, pl, ws, s))) return st;
+        return dev(ql::launch_lora_down_x(x, scaling, pl, ws, true, s, f16));
+    };
+    if (fused) {
+        // dX, and the gradient partials of each 256-token tile, from one k_dx launch
+        if (!reuse)
+            if (int st = recompute_p()) return st;
+        const ql::FusedGrads fz = ql::fused_grads_for(x, dy, pl, ws, d_lora_a != nullptr, d_lora_b != nullptr);
+        if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, true, &fz, dx_add))) return st;
+        return dev(ql::launch_fused_grads_finalize(pl, ws, d_lora_a, d_lora_b, s, f16));
+    }
+    if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, r > 0, nullptr, dx_add))) return st;
+    if (grads) {
+        if (!reuse)
+            if (int st = recompute_p()) return st;
+        if (int st = dev(ql::launch_lora_grads(x, dy, pl, ws, d_lora_a, d_lora_b, s, f16))) return st;
+    }
+    return QLORA_OK;
 }
 
 int bwd_impl(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t* codes, ql::BlockScales sc,
@@ -171,33 +226,8 @@ int bwd_impl(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t*
     const bool reuse = (flags & QLORA_BWD_REUSE_FORWARD) && T > ql::kChunkMaxT;
     if (need && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
 
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (r > 0) {
-        // s dY B^T, with the dX kernel's block scales as extra workgroups of the same launch
-        const ql::ScalesJob sj = ql::scales_job_for(sc, pl, ws);
-        if (int st = dev(ql::launch_lora_down_dy(dy, lora_b, scaling, pl, ws, grads, s, f16, &sj))) return st;
-    }
-    // s X A (both layouts) for dB when the forward's is not reused
-    auto recompute_p = [&]() -> int {
-        if (int st = dev(ql::launch_transpose_a(lora_a, pl, ws, s))) return st;
-        return dev(ql::launch_lora_down_x(x, scaling, pl, ws, true, s, f16));
-    };
-    if (fused) {
-        // dX, and the gradient partials of each 256-token tile, from one k_dx launch
-        if (!reuse)
-            if (int st = recompute_p()) return st;
-        const ql::FusedGrads fz = ql::fused_grads_for(x, dy, pl, ws, d_lora_a != nullptr, d_lora_b != nullptr);
-        if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, true, &fz))) return st;
-        return dev(ql::launch_fused_grads_finalize(pl, ws, d_lora_a, d_lora_b, s, f16));
-    }
-    if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, r > 0, nullptr))) return st;
-    if (grads) {
-        if (!reuse)
-            if (int st = recompute_p()) return st;
-        if (int st = dev(ql::launch_lora_grads(x, dy, pl, ws, d_lora_a, d_lora_b, s, f16))) return st;
-    }
-    return QLORA_OK;
+    return bwd_launch(dy, codes, sc, lora_a, lora_b, scaling, dx, nullptr, x, d_lora_a, d_lora_b, pl,
+                      static_cast<uint8_t*>(workspace), reuse, fused, static_cast<hipStream_t>(stream), f16);
 }
 
 int merge_impl(const uint8_t* codes, ql::BlockScales sc, int64_t K, int64_t N, const uint16_t* lora_a,
@@ -269,6 +299,110 @@ int quantize_dq_impl(const uint16_t* w, int64_t numel, uint8_t* codes, uint8_t* 
     if (!aligned16(w) || !aligned16(codes) || !aligned16(absmax_fp8) || !aligned16(superscale))
         return QLORA_ERR_ALIGN;
     return dev(ql::launch_quantize(w, numel, codes, absmax_fp8, superscale, static_cast<hipStream_t>(stream), f16));
+}
+
+// ------------------------------------------------------------ epilogue forward, checkpoints, their backward
+
+static_assert(QLORA_ACT_NONE == ql::kActNone && QLORA_ACT_RELU == ql::kActRelu && QLORA_ACT_SILU == ql::kActSilu &&
+                  QLORA_ACT_GELU == ql::kActGelu && QLORA_ACT_GELU_TANH == ql::kActGeluTanh,
+              "activations of the header and the kernels");
+
+int check_aligned(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return QLORA_ERR_ALIGN;
+    return QLORA_OK;
+}
+
+int act8_quantize_impl(const uint16_t* x, int64_t numel, int8_t* codes, float* scale, void* stream, bool f16) {
+    if (!x || !codes || !scale) return QLORA_ERR_NULL;
+    if (numel <= 0 || numel > kMaxNumel) return QLORA_ERR_SHAPE;
+    if (int st = check_aligned({x, codes, scale})) return st;
+    return dev(ql::launch_act8_quantize(x, numel, codes, scale, static_cast<hipStream_t>(stream), f16));
+}
+
+int act8_dequantize_impl(const int8_t* codes, const float* scale, int64_t numel, uint16_t* out, void* stream,
+                         bool f16) {
+    if (!codes || !scale || !out) return QLORA_ERR_NULL;
+    if (numel <= 0 || numel > kMaxNumel) return QLORA_ERR_SHAPE;
+    if (int st = check_aligned({codes, scale, out})) return st;
+    return dev(ql::launch_act8_dequantize(codes, scale, numel, out, static_cast<hipStream_t>(stream), f16));
+}
+
+int act_fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* codes, ql::BlockScales sc,
+                 const uint16_t* lora_a, const uint16_t* lora_b, int64_t r, float scaling, const qlora_epilogue* e,
+                 uint16_t* y, void* workspace, size_t workspace_bytes, void* stream, bool f16) {
+    if (!e || (!e->z_codes != !e->z_scale)) return QLORA_ERR_NULL;
+    if (int st = fwd_check(x, T, K, N, codes, sc, lora_a, lora_b, r, scaling, y)) return st;
+    if (int st = check_aligned({e->bias, e->mul, e->residual, e->z, e->z_codes, e->z_scale})) return st;
+    if (e->act < 0 || e->act >= ql::kActs) return QLORA_ERR_VALUE;
+    const ql::Epilogue ep{e->act, e->bias, e->mul, e->residual, e->z, e->z_codes, e->z_scale};
+    return fwd_impl(x, T, K, N, codes, sc, lora_a, lora_b, r, scaling, y, workspace, workspace_bytes, stream, f16,
+                    SIZE_MAX, &ep);
+}
+
+// Workspace of the backward from saved activations: the layer backward's own
+// regions, then dZ, X in 16 bits and the column-sum partials of the bias gradient.
+struct ActBwdPlan {
+    ql::LoraPlan pl;
+    size_t off_dz, off_x, off_part, bytes;
+    ActBwdPlan(int64_t T, int64_t K, int64_t N, int64_t r) : pl(T, K, N, r) {
+        size_t o = ql::align256(std::max(pl.bwd_grad_bytes, pl.bwd_bytes));
+        off_dz = o;   o = ql::align256(o + (size_t)T * N * 2);
+        off_x = o;    o = ql::align256(o + (r > 0 ? (size_t)T * K * 2 : 0));
+        off_part = o; o = ql::align256(o + (size_t)ql::act_bwd_ranges(T) * N * 4);
+        bytes = o;
+    }
+};
+
+int check_saved(const qlora_saved& v) {
+    if (v.values && (v.codes || v.scale)) return QLORA_ERR_VALUE;      // one form at most
+    if (!v.codes != !v.scale) return QLORA_ERR_NULL;
+    return check_aligned({v.values, v.codes, v.scale});
+}
+ql::Saved saved(const qlora_saved& v) { return {v.values, v.codes, v.scale}; }
+
+int act_bwd_impl(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t* codes, ql::BlockScales sc,
+                 const uint16_t* lora_a, const uint16_t* lora_b, int64_t r, float scaling, const qlora_act_grad* g,
+                 void* workspace, size_t workspace_bytes, void* stream, bool f16) {
+    if (!g || !dy || !codes || !scales_present(sc) || !g->dx) return QLORA_ERR_NULL;
+    if (r > 0 && (!lora_a || !lora_b)) return QLORA_ERR_NULL;
+    const bool grads = g->d_lora_a || g->d_lora_b;
+    const ql::Saved sx = saved(g->x), sz = saved(g->z), sm = saved(g->mul);
+    if (grads && !sx.present()) return QLORA_ERR_NULL;
+    if ((g->act != QLORA_ACT_NONE || g->d_mul) && !sz.present()) return QLORA_ERR_NULL;
+    if (g->d_mul && !sm.present()) return QLORA_ERR_NULL;
+    if (int st = check_linear_shape(T, K, N, r)) return st;
+    if (r == 0 && (lora_a || lora_b || grads)) return QLORA_ERR_SHAPE;
+    if (!scales_aligned(sc)) return QLORA_ERR_ALIGN;
+    for (const qlora_saved* v : {&g->x, &g->z, &g->mul})
+        if (int st = check_saved(*v)) return st;
+    if (int st = check_aligned({dy, codes, lora_a, lora_b, g->dx_add, g->dx, g->d_lora_a, g->d_lora_b, g->d_bias,
+                                g->d_mul, workspace}))
+        return st;
+    if (!std::isfinite(scaling) || g->act < 0 || g->act >= ql::kActs) return QLORA_ERR_VALUE;
+    const ActBwdPlan ap(T, K, N, r);
+    if (!workspace || workspace_bytes < ap.bytes) return QLORA_ERR_WORKSPACE;
+
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const uint16_t* dz = dy;                                           // without act and mul, dZ is dY itself
+    const bool own_dz = g->act != QLORA_ACT_NONE || sm.present();
+    if (own_dz || g->d_bias) {
+        uint16_t* out = own_dz ? reinterpret_cast<uint16_t*>(ws + ap.off_dz) : nullptr;
+        const ql::ActBwd a{g->act, dy, sz, sm, out, g->d_mul,
+                           g->d_bias ? reinterpret_cast<float*>(ws + ap.off_part) : nullptr, T, N,
+                           ql::act_bwd_rows(T)};
+        if (int st = dev(ql::launch_act_bwd(a, g->d_bias, s, f16))) return st;
+        if (own_dz) dz = out;
+    }
+    const uint16_t* x = sx.v;
+    if (grads && sx.codes) {
+        uint16_t* x16 = reinterpret_cast<uint16_t*>(ws + ap.off_x);
+        if (int st = dev(ql::launch_act8_dequantize(sx.codes, sx.scale, T * K, x16, s, f16))) return st;
+        x = x16;
+    }
+    return bwd_launch(dz, codes, sc, lora_a, lora_b, scaling, g->dx, g->dx_add, x, g->d_lora_a, g->d_lora_b, ap.pl,
+                      ws, false, false, s, f16);
 }
 
 // ------------------------------------------------------------ no-allocation forward
@@ -510,6 +644,75 @@ int qlora_linear_fwd_grouped_ex(int count, const qlora_linear_problem* problems,
 int qlora_linear_fwd_grouped(int count, const qlora_linear_problem* problems, int64_t T, int64_t r,
                              void* workspace, size_t workspace_bytes, void* stream) {
     return qlora_linear_fwd_grouped_ex(count, problems, T, r, 0u, workspace, workspace_bytes, stream);
+}
+
+int act8_quantize(const uint16_t* x, int64_t numel, int8_t* codes, float* scale, void* stream) {
+    return act8_quantize_impl(x, numel, codes, scale, stream, false);
+}
+
+int act8_quantize_f16(const uint16_t* x, int64_t numel, int8_t* codes, float* scale, void* stream) {
+    return act8_quantize_impl(x, numel, codes, scale, stream, true);
+}
+
+int act8_dequantize(const int8_t* codes, const float* scale, int64_t numel, uint16_t* x_out, void* stream) {
+    return act8_dequantize_impl(codes, scale, numel, x_out, stream, false);
+}
+
+int act8_dequantize_f16(const int8_t* codes, const float* scale, int64_t numel, uint16_t* x_out, void* stream) {
+    return act8_dequantize_impl(codes, scale, numel, x_out, stream, true);
+}
+
+int qlora_linear_act_fwd(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* codes,
+                         const uint8_t* absmax_fp8, const float* superscale, const uint16_t* lora_a, const uint16_t* lora_b,
+                         int64_t r, float scaling, const qlora_epilogue* epilogue, uint16_t* y, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return act_fwd_impl(x, T, K, N, codes, dq_scales(absmax_fp8, superscale), lora_a, lora_b, r, scaling, epilogue, y, workspace,
+                        workspace_bytes, stream, false);
+}
+
+int qlora_linear_act_bwd(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t* codes,
+                         const uint8_t* absmax_fp8, const float* superscale, const uint16_t* lora_a, const uint16_t* lora_b,
+                         int64_t r, float scaling, const qlora_act_grad* grad, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return act_bwd_impl(dy, T, K, N, codes, dq_scales(absmax_fp8, superscale), lora_a, lora_b, r, scaling, grad, workspace, workspace_bytes,
+                        stream, false);
+}
+
+int qlora_linear_act_fwd_sq(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* codes,
+                         const float* absmax, const uint16_t* lora_a, const uint16_t* lora_b,
+                         int64_t r, float scaling, const qlora_epilogue* epilogue, uint16_t* y, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return act_fwd_impl(x, T, K, N, codes, sq_scales(absmax), lora_a, lora_b, r, scaling, epilogue, y, workspace,
+                        workspace_bytes, stream, false);
+}
+
+int qlora_linear_act_bwd_sq(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t* codes,
+                         const float* absmax, const uint16_t* lora_a, const uint16_t* lora_b,
+                         int64_t r, float scaling, const qlora_act_grad* grad, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return act_bwd_impl(dy, T, K, N, codes, sq_scales(absmax), lora_a, lora_b, r, scaling, grad, workspace, workspace_bytes,
+                        stream, false);
+}
+
+int qlora_linear_act_fwd_f16(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* codes,
+                         const uint8_t* absmax_fp8, const float* superscale, const uint16_t* lora_a, const uint16_t* lora_b,
+                         int64_t r, float scaling, const qlora_epilogue* epilogue, uint16_t* y, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return act_fwd_impl(x, T, K, N, codes, dq_scales(absmax_fp8, superscale), lora_a, lora_b, r, scaling, epilogue, y, workspace,
+                        workspace_bytes, stream, true);
+}
+
+int qlora_linear_act_bwd_f16(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t* codes,
+                         const uint8_t* absmax_fp8, const float* superscale, const uint16_t* lora_a, const uint16_t* lora_b,
+                         int64_t r, float scaling, const qlora_act_grad* grad, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    return act_bwd_impl(dy, T, K, N, codes, dq_scales(absmax_fp8, superscale), lora_a, lora_b, r, scaling, grad, workspace, workspace_bytes,
+                        stream, true);
+}
+
+size_t qlora_act_workspace_bytes_bwd(int64_t T, int64_t K, int64_t N, int64_t r) {
+    if (check_linear_shape(T, K, N, r) != QLORA_OK) return 0;
+    return std::max(ActBwdPlan(T, K, N, r).bytes, fwd_workspace(T, K, N, r));
 }
 
 }  // extern "C"

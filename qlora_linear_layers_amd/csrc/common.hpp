@@ -363,13 +363,14 @@ constexpr int64_t kGemvMaxT = 16;
 // against 456 us at T = 128).
 constexpr int64_t kChunkMaxT = 96;
 struct LoraPlan;
+struct Epilogue;              // output epilogue of the forward (act.hpp); one per problem of a group, or none
 ScalesJob scales_job_for(BlockScales sc, const LoraPlan& pl, uint8_t* ws);
 size_t gemv_workspace(int64_t T, int64_t K, int64_t N, int64_t r_pad);
 hipError_t launch_merge(const uint8_t* codes, BlockScales sc, const uint16_t* lora_a, const uint16_t* lora_b,
                         int64_t K, int64_t N, int64_t r, float scaling, uint16_t* w_out, hipStream_t s, bool f16);
 hipError_t launch_gemv(const uint16_t* x, const uint8_t* codes, BlockScales sc, const uint16_t* lora_a,
                        const uint16_t* lora_b, float scaling, const LoraPlan& pl, uint8_t* ws, uint16_t* y,
-                       hipStream_t s, bool f16);
+                       hipStream_t s, bool f16, const Epilogue* epi = nullptr);
 
 // Decode forward of up to kMaxGroup independent problems in one launch pair
 // (same token count T and rank r, same storage format).
@@ -392,6 +393,6 @@ size_t gemv_group_workspace(const GemvProblem* probs, int count, int64_t T, int6
 enum class DecodeProduct { Auto, Mfma, Valu };
 constexpr int64_t kGemvValuMaxT = 8;
 hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int64_t r, uint8_t* ws, hipStream_t s,
-                             bool f16, DecodeProduct prod = DecodeProduct::Auto);
+                             bool f16, DecodeProduct prod = DecodeProduct::Auto, const Epilogue* epis = nullptr);
 
 }  // namespace ql

@@ -19,6 +19,9 @@
 // a short extra reduction at the end of each tile, from operands staged by
 // PlainRows (bf16 rows contiguous along the reduction) or TransRows (bf16
 // stored with the reduction as the row index).  Outputs leave as bf16 rows.
+#include <type_traits>
+
+#include "act.hpp"
 #include "common.hpp"
 #include "grad.hpp"
 #include "plan.hpp"
@@ -148,11 +151,32 @@ QL_DEV bf16x8_t lds_frag(const lds8_t* base, int row, int chunk) {
 QL_DEV uint32_t otile_off(int t, int c) { return (uint32_t)t * 512u + ((uint32_t)(c ^ (t & 31)) << 4); }
 
 // Columns col .. col+3 (col % 4 == 0) of tile row t: the four consecutive
-// accumulator rows of MFMA row group g.
-template <bool F16>
+// accumulator rows of MFMA row group g.  ADD: plus the values there (fp32).
+template <bool F16, bool ADD = false>
 QL_DEV void otile_put4(lds8_t* lo, const f32x16_t& v, int g, int t, int col) {
-    const u32x2_t o = {pack16x2<F16>(v[4 * g], v[4 * g + 1]), pack16x2<F16>(v[4 * g + 2], v[4 * g + 3])};
-    *reinterpret_cast<__attribute__((address_space(3))) u32x2_t*>(lo + otile_off(t, col >> 3) + (col & 7) * 2) = o;
+    auto* at = reinterpret_cast<__attribute__((address_space(3))) u32x2_t*>(lo + otile_off(t, col >> 3) + (col & 7) * 2);
+    float a = v[4 * g], b = v[4 * g + 1], c = v[4 * g + 2], d = v[4 * g + 3];
+    if constexpr (ADD) {
+        const u32x2_t q = *at;
+        a += lo16<F16>(q[0]);
+        b += hi16<F16>(q[0]);
+        c += lo16<F16>(q[1]);
+        d += hi16<F16>(q[1]);
+    }
+    *at = u32x2_t{pack16x2<F16>(a, b), pack16x2<F16>(c, d)};
+}
+
+// tile[t][c] = src[t0 + t][c0 + c] where that exists, 0 elsewhere (C % 8 == 0)
+QL_DEV void otile_load(lds8_t* lo, const uint16_t* src, int64_t lds, int64_t t0, int64_t c0, int64_t T, int64_t C) {
+#pragma unroll 8
+    for (int it = 0; it < 256 * 32 / kThreads; ++it) {
+        const int u = threadIdx.x + it * kThreads;
+        const int t = u >> 5, c = u & 31;
+        const int64_t tg = t0 + t, cg = c0 + c * 8;
+        u32x4_t v = {0, 0, 0, 0};
+        if (tg < T && cg < C) v = *reinterpret_cast<const u32x4_t*>(src + tg * lds + cg);
+        *reinterpret_cast<lds_u32x4_t*>(lo + otile_off(t, c)) = v;
+    }
 }
 
 // out[t0 + t][c0 + c] = tile[t][c] for t0 + t < T and c0 + c < C (C % 8 == 0):
@@ -389,8 +413,11 @@ QL_DEV void fwd_tile(FwdPipe<SQ>& pp, int kt, f32x16_t (&acc)[2][8], lds8_t* lX,
 // k_split_sum adds in split order.  Partial rows are padded to a multiple of
 // four tokens (ldp), so every row starts 16-byte aligned and both kernels
 // move whole float4s; the padding holds the tile's zero columns.
-template <bool SQ, bool F16, bool SPLIT>
-__global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb) {
+//
+// EPI: the tile ends in the epilogue `ep` instead of the plain rounding (a
+// split tile's epilogue runs in k_split_sum).
+template <bool SQ, bool F16, bool SPLIT, bool EPI>
+__global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epilogue ep) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     lds8_t* smem = (lds8_t*)(smem_raw);
     constexpr int TT = FwdPipe<SQ>::TT;
@@ -539,6 +566,42 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb) {
         }
         return;
     }
+    if constexpr (EPI) {
+        // C[n][t] -> fp32 rows [t][n] in LDS, 128 tokens at a time (128 KB over
+        // the X buffers and the table), so that the epilogue sees unrounded sums
+        // and moves whole rows: a lane takes eight consecutive columns of a row,
+        // 32 lanes the tile's 256.  The 16-byte chunk c of row t sits at chunk
+        // position c ^ (t & 31): the accumulator writes (consecutive lanes hold
+        // consecutive rows) spread over all banks.
+        f32x4_t* lt = reinterpret_cast<f32x4_t*>(smem_raw);              // [128][64] chunks of 4 columns
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {                                 // unrolled: acc indices stay static
+            __syncthreads();                                             // LDS readers are done
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x16_t& v = acc[i][4 * hf + jj];
+                        lt[(32 * jj + r) * 64 + ((16 * w + 8 * i + 2 * g + h) ^ r)] =
+                            f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+                    }
+            __syncthreads();
+            const int64_t n = n0 + (threadIdx.x & 31) * 8;
+#pragma unroll 2
+            for (int it = 0; it < 16; ++it) {
+                const int tl = (threadIdx.x >> 5) + 8 * it, c = 2 * (threadIdx.x & 31);
+                const int64_t t = t0 + 128 * hf + tl;
+                if (t < p.T && n < p.N) {                                // whole 64-column blocks (N % 64 == 0)
+                    const f32x4_t a = lt[tl * 64 + (c ^ (tl & 31))], b = lt[tl * 64 + ((c + 1) ^ (tl & 31))];
+                    float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                    epilogue8<F16>(ep, v, t, n, p.N, p.y);
+                }
+            }
+        }
+        return;
+    }
     // C[n][t] -> Y[t][n] through an LDS tile over the X buffers and the table
     __syncthreads();                          // every wave is done reading them
 #pragma unroll
@@ -555,10 +618,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb) {
 // adds a 64 (c) x 64 (t) block over the splits in split order (a thread four
 // consecutive t, its split loads issued four at a time), turns it in LDS and
 // stores whole 128-byte rows of out.
-template <bool F16>
+//
+// EPI: the sums stay fp32 in LDS and leave through the epilogue `ep`.
+template <bool F16, bool EPI>
 __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits, int64_t C, int64_t T,
-                                                  uint16_t* out) {
-    __shared__ uint16_t tile[64][64 + 8];             // [t][c]
+                                                  uint16_t* out, Epilogue ep) {
+    using tile_t = std::conditional_t<EPI, float, uint16_t>;
+    __shared__ tile_t tile[64][64 + (EPI ? 1 : 8)];   // [t][c]
     const int64_t c0 = (int64_t)blockIdx.x * 64, t0 = (int64_t)blockIdx.y * 64;
     const int64_t ldp = (T + 3) & ~int64_t(3);       // partial row stride (see k_fwd)
     const int64_t plane = C * ldp;
@@ -583,17 +649,28 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
             }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) tile[tl + u][cl] = (uint16_t)(pack16x2<F16>(v[u], 0.0f) & 0xFFFFu);
+        for (int u = 0; u < 4; ++u) {
+            if constexpr (EPI) tile[tl + u][cl] = v[u];
+            else tile[tl + u][cl] = (uint16_t)(pack16x2<F16>(v[u], 0.0f) & 0xFFFFu);
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 64 * 8; e += 256) {
         const int tl = e >> 3, ch = e & 7;
         const int64_t t = t0 + tl, c = c0 + ch * 8;
         if (t < T && c < C) {
-            u32x4_t v;
+            if constexpr (EPI) {
+                float v[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = (uint32_t)tile[tl][ch * 8 + 2 * q] | ((uint32_t)tile[tl][ch * 8 + 2 * q + 1] << 16);
-            *reinterpret_cast<u32x4_t*>(out + t * C + c) = v;
+                for (int q = 0; q < 8; ++q) v[q] = tile[tl][ch * 8 + q];
+                epilogue8<F16>(ep, v, t, c, C, out);
+            } else {
+                u32x4_t v;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    v[q] = (uint32_t)tile[tl][ch * 8 + 2 * q] | ((uint32_t)tile[tl][ch * 8 + 2 * q + 1] << 16);
+                *reinterpret_cast<u32x4_t*>(out + t * C + c) = v;
+            }
         }
     }
 }
@@ -612,6 +689,7 @@ struct DxArgs {
     const uint16_t* gs_lo;
     const float* sclt;        // [K/64][N] block scales c1'
     uint16_t* dx;
+    const uint16_t* dx_add;   // [T][K] added to dX before its rounding (ADD; may be dx itself)
     int64_t T, K, N, r, r_pad;
     float* part;              // split-k: fp32 partial tiles [splits][K][T rounded up to 4]
     int splits;
@@ -798,7 +876,10 @@ QL_DEV void dx_tile(DxPipe& pp, int kt, f32x16_t (&acc)[4][4], lds8_t* lW, lds8_
 // SPLIT: as in k_fwd, `splits` workgroups per tile, each over a range of the
 // reduction's n tiles (split 0 also adds the LoRA term), writing fp32
 // partial tiles that k_split_sum adds in split order.
-template <bool F16, bool FUSED, bool SPLIT>
+//
+// ADD: dX += dx_add, in fp32 before the rounding (a split tile's is added by
+// k_split_sum).
+template <bool F16, bool FUSED, bool SPLIT, bool ADD>
 __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, FusedGrads fz) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     lds8_t* smem = (lds8_t*)(smem_raw);
@@ -943,13 +1024,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
     } else {
         // C[k][t] -> dX[t][k] through an LDS tile over the W and dY tiles
         __syncthreads();                          // every wave is done reading them
+        if constexpr (ADD) {
+            // dx_add's tile goes to the same LDS tile first (whole rows); every
+            // lane then adds the four values that its sums replace
+            otile_load(smem, p.dx_add, p.K, t0, k0, p.T, p.K);
+            __syncthreads();
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                    otile_put4<F16>(smem, acc[i][j], g, wb * 128 + j * 32 + r, wa * 128 + i * 32 + g * 8 + h * 4);
+                    otile_put4<F16, ADD>(smem, acc[i][j], g, wb * 128 + j * 32 + r, wa * 128 + i * 32 + g * 8 + h * 4);
         __syncthreads();
         otile_store(smem, p.dx, p.K, t0, k0, p.T, p.K);
     }
@@ -982,10 +1069,22 @@ hipError_t set_smem(F* f, size_t bytes) {
                                (int)bytes);
 }
 
+// out[t][c] = sum of the fp32 partials of a split tile GEMM (through `epi` if given)
+hipError_t split_sum(const float* part, int splits, int64_t C, int64_t T, uint16_t* out, hipStream_t s, bool f16,
+                     const Epilogue* epi) {
+    const dim3 g((unsigned)ceil_div(C, 64), (unsigned)ceil_div(T, 64));
+    const Epilogue ep = epi ? *epi : Epilogue{};
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, g, dim3(256), 0, s, part, splits, C, T, out, ep); };
+    if (epi) f16 ? go(k_split_sum<true, true>) : go(k_split_sum<false, true>);
+    else f16 ? go(k_split_sum<true, false>) : go(k_split_sum<false, false>);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, const uint16_t* lora_b,
-                      const LoraPlan& pl, const uint8_t* ws, uint16_t* y, hipStream_t s, bool f16) {
+                      const LoraPlan& pl, const uint8_t* ws, uint16_t* y, hipStream_t s, bool f16,
+                      const Epilogue* epi) {
     const bool split = pl.s_fwd > 1;
     FwdArgs a{x, codes, sc.fp8, sc.sup, sc.absmax, lora_b, reinterpret_cast<const uint16_t*>(ws + pl.off_ps_hi),
               reinterpret_cast<const uint16_t*>(ws + pl.off_ps_lo), y,
@@ -993,24 +1092,26 @@ hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, c
               split ? reinterpret_cast<float*>(const_cast<uint8_t*>(ws) + pl.off_fsp) : nullptr, pl.s_fwd};
     const size_t lds = kFwdSmem;
     const int64_t tiles = ceil_div(pl.N, 256) * ceil_div(pl.T, 256) * (split ? pl.s_fwd : 1);
+    const Epilogue ep = epi ? *epi : Epilogue{};
     auto go = [&](auto kern) {
         hipError_t e = set_smem(kern, lds);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), lds, s, a, host_codebook());
+        hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), lds, s, a, host_codebook(), ep);
         return hipGetLastError();
     };
     if (split) {
         hipError_t e;
-        if (sc.single()) e = f16 ? go(k_fwd<true, true, true>) : go(k_fwd<true, false, true>);
-        else e = f16 ? go(k_fwd<false, true, true>) : go(k_fwd<false, false, true>);
+        if (sc.single()) e = f16 ? go(k_fwd<true, true, true, false>) : go(k_fwd<true, false, true, false>);
+        else e = f16 ? go(k_fwd<false, true, true, false>) : go(k_fwd<false, false, true, false>);
         if (e != hipSuccess) return e;
-        const dim3 g((unsigned)ceil_div(pl.N, 64), (unsigned)ceil_div(pl.T, 64));
-        if (f16) hipLaunchKernelGGL(k_split_sum<true>, g, dim3(256), 0, s, a.part, pl.s_fwd, pl.N, pl.T, y);
-        else hipLaunchKernelGGL(k_split_sum<false>, g, dim3(256), 0, s, a.part, pl.s_fwd, pl.N, pl.T, y);
-        return hipGetLastError();
+        return split_sum(a.part, pl.s_fwd, pl.N, pl.T, y, s, f16, epi);
     }
-    if (f16) return sc.single() ? go(k_fwd<true, true, false>) : go(k_fwd<false, true, false>);
-    return sc.single() ? go(k_fwd<true, false, false>) : go(k_fwd<false, false, false>);
+    if (epi) {
+        if (f16) return sc.single() ? go(k_fwd<true, true, false, true>) : go(k_fwd<false, true, false, true>);
+        return sc.single() ? go(k_fwd<true, false, false, true>) : go(k_fwd<false, false, false, true>);
+    }
+    if (f16) return sc.single() ? go(k_fwd<true, true, false, false>) : go(k_fwd<false, true, false, false>);
+    return sc.single() ? go(k_fwd<true, false, false, false>) : go(k_fwd<false, false, false, false>);
 }
 
 ScalesJob scales_job_for(BlockScales sc, const LoraPlan& pl, uint8_t* ws) {
@@ -1020,7 +1121,7 @@ ScalesJob scales_job_for(BlockScales sc, const LoraPlan& pl, uint8_t* ws) {
 
 hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, const uint16_t* lora_a,
                      const LoraPlan& pl, const uint8_t* ws, uint16_t* dx, hipStream_t s, bool f16,
-                     bool scales_ready, const FusedGrads* fused) {
+                     bool scales_ready, const FusedGrads* fused, const uint16_t* dx_add) {
     const float* sclt = reinterpret_cast<const float*>(ws + pl.off_scl);
     if (!scales_ready) {
         const ScalesJob j = scales_job_for(sc, pl, const_cast<uint8_t*>(ws));
@@ -1032,7 +1133,7 @@ hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, c
     float* part = split ? reinterpret_cast<float*>(const_cast<uint8_t*>(ws) + (fused ? pl.off_dxp_fused : pl.off_dxp))
                         : nullptr;
     DxArgs a{dy, codes, sc.fp8, sc.sup, lora_a, reinterpret_cast<const uint16_t*>(ws + pl.off_gs_hi),
-             reinterpret_cast<const uint16_t*>(ws + pl.off_gs_lo), sclt, dx,
+             reinterpret_cast<const uint16_t*>(ws + pl.off_gs_lo), sclt, dx, dx_add,
              pl.T, pl.K, pl.N, pl.r, pl.r_pad, part, pl.s_dx};
     const size_t lds = kDxSmem;
     const int64_t tiles = ceil_div(pl.K, 256) * ceil_div(pl.T, 256) * (split ? pl.s_dx : 1);
@@ -1046,16 +1147,18 @@ hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, c
     };
     hipError_t e;
     if (split) {
-        if (fused) e = f16 ? go(k_dx<true, true, true>) : go(k_dx<false, true, true>);
-        else e = f16 ? go(k_dx<true, false, true>) : go(k_dx<false, false, true>);
+        if (fused) e = f16 ? go(k_dx<true, true, true, false>) : go(k_dx<false, true, true, false>);
+        else e = f16 ? go(k_dx<true, false, true, false>) : go(k_dx<false, false, true, false>);
         if (e != hipSuccess) return e;
-        const dim3 g((unsigned)ceil_div(pl.K, 64), (unsigned)ceil_div(pl.T, 64));
-        if (f16) hipLaunchKernelGGL(k_split_sum<true>, g, dim3(256), 0, s, part, pl.s_dx, pl.K, pl.T, dx);
-        else hipLaunchKernelGGL(k_split_sum<false>, g, dim3(256), 0, s, part, pl.s_dx, pl.K, pl.T, dx);
-        return hipGetLastError();
+        const Epilogue add{kActNone, nullptr, nullptr, dx_add, nullptr, nullptr, nullptr};
+        return split_sum(part, pl.s_dx, pl.K, pl.T, dx, s, f16, dx_add ? &add : nullptr);
     }
-    if (fused) return f16 ? go(k_dx<true, true, false>) : go(k_dx<false, true, false>);
-    return f16 ? go(k_dx<true, false, false>) : go(k_dx<false, false, false>);
+    if (dx_add) {
+        if (fused) return f16 ? go(k_dx<true, true, false, true>) : go(k_dx<false, true, false, true>);
+        return f16 ? go(k_dx<true, false, false, true>) : go(k_dx<false, false, false, true>);
+    }
+    if (fused) return f16 ? go(k_dx<true, true, false, false>) : go(k_dx<false, true, false, false>);
+    return f16 ? go(k_dx<true, false, false, false>) : go(k_dx<false, false, false, false>);
 }
 
 }  // namespace ql

@@ -30,6 +30,7 @@
 // two) pays for the extra address instruction per code byte.
 #include <type_traits>
 
+#include "act.hpp"
 #include "common.hpp"
 #include "plan.hpp"
 
@@ -379,8 +380,17 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
 // CPL columns per lane: 2 up to T = 8, 1 above (more workgroups for the
 // 8-wave, 16-token case)
 constexpr int fin_cols(int64_t T) { return T <= 8 ? 128 : 64; }
-template <int TW, int CPL, bool LORA, bool F16>
-__global__ __launch_bounds__(512) void k_gemv_finalize(GemvGroup grp) {
+//
+// EPI: Y leaves through the epilogue of its problem, whose operands (bias, mul,
+// residual) are loaded with the partials; a 64-column block of a checkpoint of
+// Z is 32 lanes (CPL = 2) or the whole wave.
+struct EpiGroup {
+    Epilogue e[kMaxGroup];
+};
+struct NoEpiGroup {};
+template <int TW, int CPL, bool LORA, bool F16, bool EPI>
+__global__ __launch_bounds__(512) void k_gemv_finalize(GemvGroup grp,
+                                                       std::conditional_t<EPI, EpiGroup, NoEpiGroup> eg) {
     const int gi = group_find(grp.fin_end, grp.count, (int)blockIdx.x);
     const GemvArgs p = grp.p[gi];
     const int bx = (int)blockIdx.x - (gi ? grp.fin_end[gi - 1] : 0);
@@ -478,6 +488,22 @@ __global__ __launch_bounds__(512) void k_gemv_finalize(GemvGroup grp) {
         }
     };
 
+    // the epilogue's operands, issued first (columns n, n + 1 packed; one
+    // column in the low half)
+    [[maybe_unused]] uint32_t eb = 0, em[TW] = {}, er[TW] = {};
+    if constexpr (EPI) {
+        const Epilogue& ep = eg.e[gi];
+        auto col = [&](const uint16_t* q) -> uint32_t {
+            return CPL == 2 ? *reinterpret_cast<const uint32_t*>(q) : (uint32_t)*q;
+        };
+        if (nok && ep.bias) eb = col(ep.bias + n);
+#pragma unroll
+        for (int tw = 0; tw < TW; ++tw) {
+            const int t = wave + W * tw;
+            if (nok && t < T && ep.mul) em[tw] = col(ep.mul + (int64_t)t * p.N + n);
+            if (nok && t < T && ep.res) er[tw] = col(ep.res + (int64_t)t * p.N + n);
+        }
+    }
     uint32_t bv[LORA ? 64 : 1];
     round_t pb0, pb1;
     [[maybe_unused]] uround_t pu0, pu1;
@@ -547,6 +573,44 @@ __global__ __launch_bounds__(512) void k_gemv_finalize(GemvGroup grp) {
     for (int tw = 0; tw < TW; ++tw) {
         const int t = wave + W * tw;
         if (nok && t < T && t >= p.skip) {
+            if constexpr (EPI) {
+                const Epilogue& ep = eg.e[gi];
+                const int64_t at = (int64_t)t * p.N + n;
+                float v[CPL];
+#pragma unroll
+                for (int e = 0; e < CPL; ++e) {
+                    v[e] = y[tw][e];
+                    if (ep.bias) v[e] += e ? hi16<F16>(eb) : lo16<F16>(eb);
+                }
+                if (ep.z || ep.zc) {
+                    const uint32_t zq = pack16x2<F16>(v[0], CPL == 2 ? v[CPL - 1] : 0.0f);
+                    if (ep.z) {
+                        if constexpr (CPL == 2) *reinterpret_cast<uint32_t*>(ep.z + at) = zq;
+                        else ep.z[at] = (uint16_t)zq;
+                    }
+                    if (ep.zc) {
+                        uint32_t m = max_of_8_lanes(abs_max2(zq, 0));
+                        m = max(m, (uint32_t)__shfl_xor((int)m, 8));
+                        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+                        if constexpr (CPL == 1) m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+                        float d, inv;
+                        ck_scale<F16>(m, d, inv);
+                        const uint32_t q0 = ck_code(lo16<F16>(zq), inv) & 0xFFu;
+                        if constexpr (CPL == 2)
+                            *reinterpret_cast<uint16_t*>(ep.zc + at) =
+                                (uint16_t)(q0 | (ck_code(hi16<F16>(zq), inv) & 0xFFu) << 8);
+                        else ep.zc[at] = (int8_t)q0;
+                        if ((n & 63) == 0) ep.zs[at >> 6] = d;
+                    }
+                }
+                act_values(ep.act, v);
+#pragma unroll
+                for (int e = 0; e < CPL; ++e) {
+                    if (ep.mul) v[e] *= e ? hi16<F16>(em[tw]) : lo16<F16>(em[tw]);
+                    if (ep.res) v[e] += e ? hi16<F16>(er[tw]) : lo16<F16>(er[tw]);
+                    y[tw][e] = v[e];
+                }
+            }
             if constexpr (CPL == 2)
                 *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.N + n) = pack16x2<F16>(y[tw][0], y[tw][1]);
             else
@@ -569,7 +633,7 @@ size_t gemv_group_workspace(const GemvProblem* probs, int count, int64_t T, int6
 }
 
 hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int64_t r, uint8_t* ws, hipStream_t s,
-                             bool f16, DecodeProduct prod) {
+                             bool f16, DecodeProduct prod, const Epilogue* epis) {
     if (count < 1 || count > kMaxGroup) return hipErrorInvalidValue;
     if (prod == DecodeProduct::Valu && T > kGemvValuMaxT) return hipErrorInvalidValue;
     const bool dot = prod == DecodeProduct::Valu;
@@ -630,11 +694,23 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     // for T > 8 (two tokens each); every wave loads the B column itself
     const int fw = T <= 4 ? (int)T : T <= 8 ? 4 : 8;
     const dim3 fg((unsigned)nfin), fb((unsigned)(64 * fw));
-    auto fin = [&](auto kern) { hipLaunchKernelGGL(kern, fg, fb, 0, s, g); };
-    auto fin_tw = [&](auto tw, auto cpl) {
+    auto fin_epi = [&](auto tw, auto cpl, auto epi, const auto& eg) {
         constexpr int TW = decltype(tw)::value, CPL = decltype(cpl)::value;
-        if (r_pad > 0) f16 ? fin(k_gemv_finalize<TW, CPL, true, true>) : fin(k_gemv_finalize<TW, CPL, true, false>);
-        else f16 ? fin(k_gemv_finalize<TW, CPL, false, true>) : fin(k_gemv_finalize<TW, CPL, false, false>);
+        constexpr bool E = decltype(epi)::value;
+        auto fin = [&](auto kern) { hipLaunchKernelGGL(kern, fg, fb, 0, s, g, eg); };
+        if (r_pad > 0)
+            f16 ? fin(k_gemv_finalize<TW, CPL, true, true, E>) : fin(k_gemv_finalize<TW, CPL, true, false, E>);
+        else
+            f16 ? fin(k_gemv_finalize<TW, CPL, false, true, E>) : fin(k_gemv_finalize<TW, CPL, false, false, E>);
+    };
+    auto fin_tw = [&](auto tw, auto cpl) {
+        if (epis) {
+            EpiGroup eg{};
+            for (int i = 0; i < count; ++i) eg.e[i] = epis[i];
+            fin_epi(tw, cpl, std::true_type{}, eg);
+        } else {
+            fin_epi(tw, cpl, std::false_type{}, NoEpiGroup{});
+        }
     };
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
@@ -646,9 +722,9 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
 
 hipError_t launch_gemv(const uint16_t* x, const uint8_t* codes, BlockScales sc, const uint16_t* lora_a,
                        const uint16_t* lora_b, float scaling, const LoraPlan& pl, uint8_t* ws, uint16_t* y,
-                       hipStream_t s, bool f16) {
+                       hipStream_t s, bool f16, const Epilogue* epi) {
     const GemvProblem q{x, codes, sc, lora_a, lora_b, scaling, pl.K, pl.N, y};
-    return launch_gemv_group(&q, 1, pl.T, pl.r, ws, s, f16);
+    return launch_gemv_group(&q, 1, pl.T, pl.r, ws, s, f16, DecodeProduct::Auto, epi);
 }
 
 }  // namespace ql
