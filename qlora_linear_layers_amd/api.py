@@ -7,6 +7,7 @@ names match the C entry points.  A missing library raises ``RuntimeError``;
 there is no fallback.
 """
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 
@@ -139,11 +140,13 @@ def _check(fn, status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """Handle of torch's current stream on the current device (0 is the default stream).  The raw
+    getters cost 0.2 us against 2.7 us for torch.cuda.current_stream(), which builds a Stream."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t, dtype, name):
@@ -177,9 +180,15 @@ def _entry(stem, ct, qw):
 
 
 def _shape(t, shape, name):
-    """Raise ValueError unless tensor `t` (if given) has exactly `shape`."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    """Raise ValueError unless tensor `t` (if given) has exactly `shape` (a tuple)."""
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _count(t, n, name):
+    """Raise ValueError unless tensor `t` holds exactly `n` elements, in any shape."""
+    if t.numel() != n:
+        raise ValueError(f"{name} has shape {(t.numel(),)}, expected {(n,)}")
 
 
 def _check_storage(qw):
@@ -188,12 +197,12 @@ def _check_storage(qw):
     n = qw.N * qw.K
     if qw.N < 1 or qw.K < 1 or n % 64:
         raise ValueError(f"quantized weight [{qw.N}, {qw.K}]: N*K must be a positive multiple of 64")
-    _shape(qw.codes.reshape(-1), (n // 2,), "codes")
+    _count(qw.codes, n // 2, "codes")
     if isinstance(qw, NF4WeightSQ):
-        _shape(qw.absmax.reshape(-1), (n // 64,), "absmax")
+        _count(qw.absmax, n // 64, "absmax")
     else:
-        _shape(qw.absmax_fp8.reshape(-1), (n // 64,), "absmax_fp8")
-        _shape(qw.superscale.reshape(-1), (-(-n // 16384),), "superscale")
+        _count(qw.absmax_fp8, n // 64, "absmax_fp8")
+        _count(qw.superscale, -(-n // 16384), "superscale")
 
 
 def _check_adapters(lora_a, lora_b, K, N):
@@ -603,10 +612,7 @@ class Act8:
 
     @property
     def numel(self):
-        n = 1
-        for d in self.shape:
-            n *= d
-        return n
+        return math.prod(self.shape)
 
     def nbytes(self):
         return self.codes.numel() + 4 * self.scale.numel()
@@ -614,15 +620,14 @@ class Act8:
 
 def _check_act8(a8, name):
     """The checkpoint's tensors must hold exactly what its shape needs."""
-    _shape(a8.codes.reshape(-1), (a8.numel,), f"{name} codes")
-    _shape(a8.scale.reshape(-1), (-(-a8.numel // 64),), f"{name} scale")
+    n = a8.numel
+    _count(a8.codes, n, f"{name} codes")
+    _count(a8.scale, -(-n // 64), f"{name} scale")
 
 
 def act8_empty(shape, device="cuda"):
     """An Act8 of uninitialised storage for an activation of `shape`."""
-    n = 1
-    for d in shape:
-        n *= d
+    n = math.prod(shape)
     return Act8(torch.empty(n, dtype=torch.int8, device=device),
                 torch.empty(-(-n // 64), dtype=torch.float32, device=device), tuple(shape))
 

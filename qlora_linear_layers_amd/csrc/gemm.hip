@@ -407,6 +407,39 @@ QL_DEV void fwd_tile(FwdPipe<SQ>& pp, int kt, f32x16_t (&acc)[2][8], lds8_t* lX,
     c1p[1] = n1p[1];
 }
 
+// The epilogue's operands of one 256 x 256 tile: lane l takes columns
+// 8 (l % 32) .. +7 of row l / 32 + 8 i of each 128-row half, sixteen rows in
+// groups of kGrp, one group ahead of the rows in work (two register sets).
+// An absent operand has an empty buffer and reads zeros without a memory
+// access, and so do rows and columns past the end.
+struct EpiPipe {
+    static constexpr int kGrp = 4, kGroups = 16 / kGrp;
+    rsrc_t rm, rr;
+    uint32_t off0;
+    int64_t row2, left;                       // bytes of a row; rows from the tile's first to the last
+    u32x4_t bq, mq[2][kGrp], rq[2][kGrp];
+
+    static QL_DEV int row(int q, int u) { return (int)(threadIdx.x >> 5) + 8 * (q * kGrp + u); }
+    QL_DEV void init(const Epilogue& ep, int64_t T, int64_t N, int64_t t0, int64_t n0) {
+        const int64_t n = n0 + (threadIdx.x & 31) * 8;
+        rm = make_rsrc(ep.mul, ep.mul ? T * N * 2 : 0);
+        rr = make_rsrc(ep.res, ep.res ? T * N * 2 : 0);
+        bq = bload16(make_rsrc(ep.bias, ep.bias ? N * 2 : 0), n < N ? (uint32_t)(n * 2) : kOOB, 0);
+        row2 = N * 2;
+        off0 = (uint32_t)((t0 * N + n) * 2);
+        left = n < N ? T - t0 : 0;
+    }
+    QL_DEV void load(int hf, int q, int slot) {
+#pragma unroll
+        for (int u = 0; u < kGrp; ++u) {
+            const int t = 128 * hf + row(q, u);
+            const uint32_t vo = t < left && hf < 2 ? off0 + (uint32_t)(t * row2) : kOOB;
+            mq[slot][u] = bload16(rm, vo, 0);
+            rq[slot][u] = bload16(rr, vo, 0);
+        }
+    }
+};
+
 // SPLIT: the grid holds `splits` workgroups per tile; workgroup (tile,
 // split) takes k tiles [split KT / splits, (split + 1) KT / splits) (split 0
 // also the LoRA term) and stores its fp32 tile in part[split][n][t], which
@@ -503,6 +536,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
     }
     if (kt < KT) fwd_tile<0, SQ, F16>(pp, kt, acc, lX, r, h, xa, aa, qa, c1p);
 
+    [[maybe_unused]] EpiPipe eo;
+    if constexpr (EPI) {                      // the first rows' operands arrive during the LoRA term
+        eo.init(ep, p.T, p.N, t0, n0);
+        eo.load(0, 0, 0);
+    }
     if (p.r > 0 && split == 0) {
         // reduction over [hi | lo] of s X A (tokens) against B^T stacked twice (rows n)
         TransRows<256> pl;
@@ -572,32 +610,48 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
         // and moves whole rows: a lane takes eight consecutive columns of a row,
         // 32 lanes the tile's 256.  The 16-byte chunk c of row t sits at chunk
         // position c ^ (t & 31): the accumulator writes (consecutive lanes hold
-        // consecutive rows) spread over all banks.
+        // consecutive rows) spread over all banks.  The loops stay rolled around
+        // groups of kGrp rows per lane, so that the code of the activations is
+        // not repeated for every row.
         f32x4_t* lt = reinterpret_cast<f32x4_t*>(smem_raw);              // [128][64] chunks of 4 columns
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {                                 // unrolled: acc indices stay static
+        const int64_t n = n0 + (threadIdx.x & 31) * 8;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
             __syncthreads();                                             // LDS readers are done
+            auto stage = [&](auto first) {                               // static accumulator indices
+                constexpr int J0 = decltype(first)::value;
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
+                for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const f32x16_t& v = acc[i][4 * hf + jj];
-                        lt[(32 * jj + r) * 64 + ((16 * w + 8 * i + 2 * g + h) ^ r)] =
-                            f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-                    }
+                        for (int g = 0; g < 4; ++g) {
+                            const f32x16_t& v = acc[i][J0 + jj];
+                            lt[(32 * jj + r) * 64 + ((16 * w + 8 * i + 2 * g + h) ^ r)] =
+                                f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+                        }
+            };
+            if (hf == 0) stage(std::integral_constant<int, 0>{});
+            else stage(std::integral_constant<int, 4>{});
             __syncthreads();
-            const int64_t n = n0 + (threadIdx.x & 31) * 8;
-#pragma unroll 2
-            for (int it = 0; it < 16; ++it) {
-                const int tl = (threadIdx.x >> 5) + 8 * it, c = 2 * (threadIdx.x & 31);
-                const int64_t t = t0 + 128 * hf + tl;
-                if (t < p.T && n < p.N) {                                // whole 64-column blocks (N % 64 == 0)
+            auto rows = [&](int q, int slot) {                           // group q of this half
+#pragma unroll
+                for (int u = 0; u < EpiPipe::kGrp; ++u) {
+                    const int tl = EpiPipe::row(q, u), c = 2 * (threadIdx.x & 31);
+                    const int64_t t = t0 + 128 * hf + tl;
                     const f32x4_t a = lt[tl * 64 + (c ^ (tl & 31))], b = lt[tl * 64 + ((c + 1) ^ (tl & 31))];
                     float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-                    epilogue8<F16>(ep, v, t, n, p.N, p.y);
+                    if (t < p.T && n < p.N)                              // whole 64-column blocks (N % 64 == 0)
+                        epilogue8<F16>(ep, v, eo.bq, eo.mq[slot][u], eo.rq[slot][u], t, n, p.N, p.y);
                 }
+            };
+#pragma unroll 1
+            for (int q = 0; q < EpiPipe::kGroups; q += 2) {
+                eo.load(hf, q + 1, 1);
+                rows(q, 0);
+                if (q + 2 < EpiPipe::kGroups) eo.load(hf, q + 2, 0);
+                else eo.load(hf + 1, 0, 0);                              // past the tile: reads nothing
+                rows(q + 1, 1);
             }
         }
         return;
@@ -628,6 +682,20 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
     const int64_t c0 = (int64_t)blockIdx.x * 64, t0 = (int64_t)blockIdx.y * 64;
     const int64_t ldp = (T + 3) & ~int64_t(3);       // partial row stride (see k_fwd)
     const int64_t plane = C * ldp;
+    // the epilogue's operands for this thread's two row chunks, ahead of the sums
+    [[maybe_unused]] u32x4_t bq = {}, mq[2] = {}, rq[2] = {};
+    if constexpr (EPI) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int e = (int)threadIdx.x + 256 * k;
+            const int64_t t = t0 + (e >> 3), c = c0 + (e & 7) * 8;
+            if (t < T && c < C) {
+                if (ep.mul) mq[k] = *reinterpret_cast<const u32x4_t*>(ep.mul + t * C + c);
+                if (ep.res) rq[k] = *reinterpret_cast<const u32x4_t*>(ep.res + t * C + c);
+                if (ep.bias) bq = *reinterpret_cast<const u32x4_t*>(ep.bias + c);
+            }
+        }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int e = (int)threadIdx.x + 256 * k;     // 64 rows c x 16 float4 of t
@@ -655,7 +723,9 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 64 * 8; e += 256) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = (int)threadIdx.x + 256 * k;
         const int tl = e >> 3, ch = e & 7;
         const int64_t t = t0 + tl, c = c0 + ch * 8;
         if (t < T && c < C) {
@@ -663,7 +733,7 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* part, int splits
                 float v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = tile[tl][ch * 8 + q];
-                epilogue8<F16>(ep, v, t, c, C, out);
+                epilogue8<F16>(ep, v, bq, mq[k], rq[k], t, c, C, out);
             } else {
                 u32x4_t v;
 #pragma unroll
