@@ -96,86 +96,131 @@ __global__ __launch_bounds__(kThreads) void k_act8_dequantize(const int8_t* __re
 
 namespace {
 
-// eight values of a saved [T][N] activation at element `at` (at % 8 == 0)
-template <bool F16>
-QL_DEV void saved8(const Saved& s, int64_t at, float (&v)[8]) {
-    if (s.codes) {
-        const u32x2_t c = *reinterpret_cast<const u32x2_t*>(s.codes + at);
-        const float d = s.scale[at >> 6];
-        ck_values4(c[0], d, v);
-        ck_values4(c[1], d, v + 4);
-    } else {
-        unpack8<F16>(*reinterpret_cast<const u32x4_t*>(s.v + at), v);
+// A saved activation as buffers: 16-bit values, or codes and scales; an absent
+// one has empty buffers and reads zeros.  Eight values at element `at`
+// (a multiple of 8), loaded raw and turned into fp32 later.
+struct SavedRow {
+    u32x4_t q;                // 16-bit values, or the codes in the first two dwords
+    uint32_t d;
+};
+struct SavedBuf {
+    rsrc_t rv, rd;
+    bool q8;
+    QL_DEV SavedBuf(const Saved& s, int64_t numel) : q8(s.codes != nullptr) {
+        rv = q8 ? make_rsrc(s.codes, numel) : make_rsrc(s.v, s.v ? numel * 2 : 0);
+        rd = make_rsrc(s.scale, q8 ? numel / 16 : 0);
     }
-}
+    QL_DEV SavedRow load(bool ok, uint32_t at) const {
+        SavedRow r;
+        if (q8) {
+            const u32x2_t c = bload8(rv, ok ? at : kOOB, 0);
+            r.q = u32x4_t{c[0], c[1], 0, 0};
+            r.d = bload4(rd, ok ? at / 64 * 4 : kOOB, 0);
+        } else {
+            r.q = bload16(rv, ok ? at * 2 : kOOB, 0);
+            r.d = 0;
+        }
+        return r;
+    }
+    template <bool F16>
+    QL_DEV void values(const SavedRow& r, float (&v)[8]) const {
+        if (q8) {
+            ck_values4(r.q[0], __uint_as_float(r.d), v);
+            ck_values4(r.q[1], __uint_as_float(r.d), v + 4);
+        } else {
+            unpack8<F16>(r.q, v);
+        }
+    }
+};
 
 }  // namespace
 
-// A workgroup owns 128 columns (16 lanes of 8) and one range of rows, 16 rows
-// per step.  Column sums stay in registers over the steps; the 16 row slots of
-// a column are then added in LDS in slot order, so d_bias is deterministic.
+// A workgroup owns 128 columns (16 lanes of 8) and one range of rows, 16 row
+// slots of four rows each per step: the loads of a step's four rows are all
+// issued before the first is used.  Column sums stay in registers over the
+// steps; the 16 row slots of a column are then added in LDS in slot order, so
+// d_bias is deterministic.
 template <int ACT, bool F16>
-__global__ __launch_bounds__(kThreads) void k_act_bwd(ActBwd a) {
+QL_DEV void act_bwd_block(const ActBwd& a, int bid, float* red) {
+    constexpr int U = 4;
+    const int cb = (int)ceil_div(a.N, 128);
+    const int bx = bid % cb, by = bid / cb;
     const int cl = threadIdx.x & 15, slot = threadIdx.x >> 4;
-    const int64_t n = (int64_t)blockIdx.x * 128 + cl * 8;
-    const int64_t r0 = (int64_t)blockIdx.y * a.rows;
+    const int64_t n = (int64_t)bx * 128 + cl * 8;
+    const int64_t r0 = (int64_t)by * a.rows;
     const int64_t r1 = r0 + a.rows < a.T ? r0 + a.rows : a.T;
     const bool nok = n < a.N;
-    const bool has_z = a.z.v || a.z.codes, has_mul = a.mul.v || a.mul.codes;
+    const bool has_mul = a.mul.v || a.mul.codes;
+    const rsrc_t rdy = make_rsrc(a.dy, a.T * a.N * 2);
+    const SavedBuf zb(a.z, a.T * a.N), ub(a.mul, a.T * a.N);
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-    if (nok) {
-#pragma unroll 2
-        for (int64_t t = r0 + slot; t < r1; t += 16) {
-            const int64_t at = t * a.N + n;
-            float dy[8], z[8], u[8];
-            unpack8<F16>(*reinterpret_cast<const u32x4_t*>(a.dy + at), dy);
-            if (has_z) {
-                saved8<F16>(a.z, at, z);
-            } else {
+#pragma unroll 1
+    for (int64_t t0 = r0 + slot; t0 < r1; t0 += 16 * U) {
+        u32x4_t dyq[U];
+        SavedRow zr[U], ur[U];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = 0.0f;
-            }
-            if (has_mul) saved8<F16>(a.mul, at, u);
-            float h[8];
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + 16 * u;
+            const bool ok = nok && t < r1;
+            const uint32_t at = (uint32_t)(t * a.N + n);
+            dyq[u] = bload16(rdy, ok ? at * 2 : kOOB, 0);
+            zr[u] = zb.load(ok, at);
+            ur[u] = ub.load(ok, at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + 16 * u;
+            const bool ok = nok && t < r1;
+            float dy[8], z[8], m[8], h[8];
+            unpack8<F16>(dyq[u], dy);
+            zb.template values<F16>(zr[u], z);
+            if (has_mul) ub.template values<F16>(ur[u], m);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float d;
                 act_slope<ACT>(z[e], h[e], d);
                 h[e] *= dy[e];
-                if (has_mul) dy[e] *= u[e];
+                if (has_mul) dy[e] *= m[e];
                 dy[e] *= d;
                 sum[e] += dy[e];
             }
-            if (a.dmul) *reinterpret_cast<u32x4_t*>(a.dmul + at) = pack8<F16>(h);
-            if (a.dz) *reinterpret_cast<u32x4_t*>(a.dz + at) = pack8<F16>(dy);
+            if (ok) {
+                if (a.dmul) *reinterpret_cast<u32x4_t*>(a.dmul + t * a.N + n) = pack8<F16>(h);
+                if (a.dz) *reinterpret_cast<u32x4_t*>(a.dz + t * a.N + n) = pack8<F16>(dy);
+            }
         }
     }
     if (!a.part) return;
-    __shared__ float red[16][128 + 4];
+    constexpr int kRow = 128 + 4;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[slot][cl * 8 + e] = sum[e];
+    for (int e = 0; e < 8; ++e) red[slot * kRow + cl * 8 + e] = sum[e];
     __syncthreads();
     if (threadIdx.x < 128) {
-        const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
-        float v = red[0][threadIdx.x];
+        const int64_t c = (int64_t)bx * 128 + threadIdx.x;
+        float v = red[threadIdx.x];
 #pragma unroll
-        for (int q = 1; q < 16; ++q) v += red[q][threadIdx.x];
-        if (c < a.N) a.part[(int64_t)blockIdx.y * a.N + c] = v;
+        for (int q = 1; q < 16; ++q) v += red[q * kRow + threadIdx.x];
+        if (c < a.N) a.part[(int64_t)by * a.N + c] = v;
     }
 }
 
-// d_bias[n] = RNE_16(sum over the row ranges, in range order)
+constexpr int kActBwdLds = kTransposeLds > 16 * 132 * 4 ? kTransposeLds : 16 * 132 * 4;
+static_assert(kScalesLds <= kActBwdLds, "the jobs share the workgroup's LDS");
+
+template <int ACT, bool F16>
+__global__ __launch_bounds__(kThreads) void k_act_bwd(ActBwd a, ScalesJob sj, TransposeJob tj) {
+    __shared__ __align__(16) uint8_t lds[kActBwdLds];
+    const int bid = (int)blockIdx.x;
+    if (bid < a.blocks) act_bwd_block<ACT, F16>(a, bid, reinterpret_cast<float*>(lds));
+    else if (bid < a.blocks + sj.blocks) scales_job(sj, bid - a.blocks, (lds8_t*)lds);
+    else transpose_job(tj, bid - a.blocks - sj.blocks, (lds8_t*)lds);
+}
+
 template <bool F16>
-__global__ __launch_bounds__(kThreads) void k_bias_fin(const float* __restrict__ part, int64_t ranges, int64_t N,
-                                                       uint16_t* __restrict__ out) {
-    const int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (n >= N) return;
-    float v = 0.0f;
-#pragma unroll 8
-    for (int64_t q = 0; q < ranges; ++q) v += part[q * N + n];
-    out[n] = (uint16_t)(pack16x2<F16>(v, 0.0f) & 0xFFFFu);
+__global__ __launch_bounds__(kThreads) void k_bias_fin(BiasFin b) {
+    bias_fin<F16>(b, (int)blockIdx.x);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -196,10 +241,10 @@ hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64
     return hipGetLastError();
 }
 
-hipError_t launch_act_bwd(const ActBwd& a, uint16_t* d_bias, hipStream_t s, bool f16) {
-    const int64_t ranges = ceil_div(a.T, a.rows);
-    const dim3 g((unsigned)ceil_div(a.N, 128), (unsigned)ranges);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, g, dim3(kThreads), 0, s, a); };
+hipError_t launch_act_bwd(const ActBwd& a, const ScalesJob& sj, const TransposeJob& tj, hipStream_t s, bool f16) {
+    const int n = a.blocks + sj.blocks + tj.blocks;
+    if (n == 0) return hipSuccess;
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(kThreads), 0, s, a, sj, tj); };
     switch (a.act) {
         case kActRelu: f16 ? go(k_act_bwd<kActRelu, true>) : go(k_act_bwd<kActRelu, false>); break;
         case kActSilu: f16 ? go(k_act_bwd<kActSilu, true>) : go(k_act_bwd<kActSilu, false>); break;
@@ -207,11 +252,13 @@ hipError_t launch_act_bwd(const ActBwd& a, uint16_t* d_bias, hipStream_t s, bool
         case kActGeluTanh: f16 ? go(k_act_bwd<kActGeluTanh, true>) : go(k_act_bwd<kActGeluTanh, false>); break;
         default: f16 ? go(k_act_bwd<kActNone, true>) : go(k_act_bwd<kActNone, false>); break;
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !d_bias) return e;
-    const dim3 bg((unsigned)ceil_div(a.N, kThreads));
-    if (f16) hipLaunchKernelGGL(k_bias_fin<true>, bg, dim3(kThreads), 0, s, a.part, ranges, a.N, d_bias);
-    else hipLaunchKernelGGL(k_bias_fin<false>, bg, dim3(kThreads), 0, s, a.part, ranges, a.N, d_bias);
+    return hipGetLastError();
+}
+
+hipError_t launch_bias_fin(const BiasFin& b, hipStream_t s, bool f16) {
+    const dim3 g((unsigned)bias_fin_blocks(b));
+    if (f16) hipLaunchKernelGGL(k_bias_fin<true>, g, dim3(kThreads), 0, s, b);
+    else hipLaunchKernelGGL(k_bias_fin<false>, g, dim3(kThreads), 0, s, b);
     return hipGetLastError();
 }
 

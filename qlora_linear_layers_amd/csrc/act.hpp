@@ -167,22 +167,6 @@ QL_DEV void ck_values4(uint32_t codes, float d, float* v) {
     for (int e = 0; e < 4; ++e) v[e] = (float)(int8_t)(codes >> (8 * e)) * d;
 }
 
-// ------------------------------------------------------------------ epilogue of the forward
-
-// Z = product + bias, Y = act(Z) * mul + residual, all in fp32 with one
-// rounding at each output.  z: Z in 16 bits; zc / zs: the checkpoint of that
-// 16-bit Z.  Y may be the buffer of mul or residual (every element is read
-// before the same thread writes it).
-struct Epilogue {
-    int act;
-    const uint16_t* bias;     // [N], or null (as the other pointers)
-    const uint16_t* mul;      // [T][N]
-    const uint16_t* res;      // [T][N]
-    uint16_t* z;              // [T][N]
-    int8_t* zc;               // [T][N]
-    float* zs;                // [T][N / 64]
-};
-
 template <bool F16>
 QL_DEV u32x4_t pack8(const float (&v)[8]) {
     u32x4_t o;
@@ -198,6 +182,32 @@ QL_DEV void unpack8(const u32x4_t& q, float (&v)[8]) {
         v[2 * p + 1] = hi16<F16>(q[p]);
     }
 }
+
+// RNE_16(fl32(q d)) of eight codes: the operand that a checkpoint puts into a
+// matrix product
+template <bool F16>
+QL_DEV u32x4_t ck_pack8(const u32x2_t& codes, float d) {
+    float v[8];
+    ck_values4(codes[0], d, v);
+    ck_values4(codes[1], d, v + 4);
+    return pack8<F16>(v);
+}
+
+// ------------------------------------------------------------------ epilogue of the forward
+
+// Z = product + bias, Y = act(Z) * mul + residual, all in fp32 with one
+// rounding at each output.  z: Z in 16 bits; zc / zs: the checkpoint of that
+// 16-bit Z.  Y may be the buffer of mul or residual (every element is read
+// before the same thread writes it).
+struct Epilogue {
+    int act;
+    const uint16_t* bias;     // [N], or null (as the other pointers)
+    const uint16_t* mul;      // [T][N]
+    const uint16_t* res;      // [T][N]
+    uint16_t* z;              // [T][N]
+    int8_t* zc;               // [T][N]
+    float* zs;                // [T][N / 64]
+};
 
 // The epilogue of eight consecutive columns n .. n + 7 of row t (n % 8 == 0):
 // product sums in v, the operands' eight 16-bit values in bq, mq, rq (unused
@@ -261,21 +271,48 @@ struct ActBwd {
     uint16_t* dz;
     uint16_t* dmul;
     float* part;
-    int64_t T, N, rows;       // rows: rows of one range (a multiple of 16)
+    int64_t T, N, rows;       // rows: rows of one range (a multiple of 64)
+    int blocks;               // workgroups of the elementwise pass, 0 = none
 };
 
+// Rows of one range: enough workgroups (128 columns each) for four a CU, at
+// most 64 ranges with a bias gradient (its partials are summed range by range).
 constexpr int64_t kActBwdMaxRanges = 64;
-// rows of one range: 128, or enough that there are at most kActBwdMaxRanges
-inline int64_t act_bwd_rows(int64_t T) {
-    const int64_t r = (T + kActBwdMaxRanges - 1) / kActBwdMaxRanges;
-    return r <= 128 ? 128 : (r + 15) / 16 * 16;
+inline int64_t act_bwd_rows(int64_t T, int64_t N) {
+    const int64_t cb = (N + 127) / 128;
+    int64_t r = T * cb / 1024 / 64 * 64;
+    if (r < 64) r = 64;
+    const int64_t least = ((T + kActBwdMaxRanges - 1) / kActBwdMaxRanges + 63) / 64 * 64;
+    return r > least ? r : least;
 }
-inline int64_t act_bwd_ranges(int64_t T) { return (T + act_bwd_rows(T) - 1) / act_bwd_rows(T); }
+inline int64_t act_bwd_ranges(int64_t T, int64_t N) {
+    return (T + act_bwd_rows(T, N) - 1) / act_bwd_rows(T, N);
+}
+
+// d_bias[n] = RNE_16 of the sum of part[range][n] in range order, 256 columns
+// per workgroup
+struct BiasFin {
+    const float* part;
+    int64_t ranges, N;
+    uint16_t* out;            // null = no job
+};
+inline int bias_fin_blocks(const BiasFin& b) { return b.out ? (int)((b.N + 255) / 256) : 0; }
+template <bool F16>
+QL_DEV void bias_fin(const BiasFin& b, int bid) {
+    const int64_t n = (int64_t)bid * 256 + threadIdx.x;
+    if (n >= b.N) return;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int64_t q = 0; q < b.ranges; ++q) v += b.part[q * b.N + n];
+    b.out[n] = (uint16_t)(pack16x2<F16>(v, 0.0f) & 0xFFFFu);
+}
 
 hipError_t launch_act8_quantize(const uint16_t* x, int64_t numel, int8_t* codes, float* scale, hipStream_t s, bool f16);
 hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64_t numel, uint16_t* out, hipStream_t s,
                                   bool f16);
-// the elementwise pass, then d_bias from the partials (when asked for)
-hipError_t launch_act_bwd(const ActBwd& a, uint16_t* d_bias, hipStream_t s, bool f16);
+// the elementwise pass, with the block scales and A^T of the products behind it
+// as extra workgroups of the same launch (any of the three may be absent)
+hipError_t launch_act_bwd(const ActBwd& a, const ScalesJob& sj, const TransposeJob& tj, hipStream_t s, bool f16);
+hipError_t launch_bias_fin(const BiasFin& b, hipStream_t s, bool f16);
 
 }  // namespace ql

@@ -25,7 +25,10 @@ hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, c
 hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, const uint16_t* lora_a,
                      const LoraPlan& pl, const uint8_t* ws, uint16_t* dx, hipStream_t s, bool f16,
                      bool scales_ready, const FusedGrads* fused, const uint16_t* dx_add);
-hipError_t launch_lora_grads(const uint16_t* x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws,
+hipError_t launch_lora_down_pair(const uint16_t* dz, const uint16_t* lora_b, const Saved& x, float scaling,
+                                 const LoraPlan& pl, uint8_t* ws, float* xpart, const BiasFin& bf, hipStream_t s,
+                                 bool f16);
+hipError_t launch_lora_grads(const Saved& x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws,
                              uint16_t* d_lora_a, uint16_t* d_lora_b, hipStream_t s, bool f16);
 FusedGrads fused_grads_for(const uint16_t* x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws, bool da,
                            bool db);
@@ -167,10 +170,10 @@ int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
     return dev(ql::launch_fwd(x, codes, sc, lora_b, pl, ws, y, s, f16, epi));
 }
 
-// Launch sequence of the backward (arguments checked): dX (plus dx_add if
-// given), and dA, dB where asked for.
+// Launch sequence of the backward (arguments checked): dX, and dA, dB where
+// asked for.
 int bwd_launch(const uint16_t* dy, const uint8_t* codes, ql::BlockScales sc, const uint16_t* lora_a,
-               const uint16_t* lora_b, float scaling, uint16_t* dx, const uint16_t* dx_add, const uint16_t* x,
+               const uint16_t* lora_b, float scaling, uint16_t* dx, const uint16_t* x,
                uint16_t* d_lora_a, uint16_t* d_lora_b, const ql::LoraPlan& pl, uint8_t* ws, bool reuse, bool fused,
                hipStream_t s, bool f16) {
     const int64_t r = pl.r;
@@ -190,14 +193,14 @@ int bwd_launch(const uint16_t* dy, const uint8_t* codes, ql::BlockScales sc, con
         if (!reuse)
             if (int st = recompute_p()) return st;
         const ql::FusedGrads fz = ql::fused_grads_for(x, dy, pl, ws, d_lora_a != nullptr, d_lora_b != nullptr);
-        if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, true, &fz, dx_add))) return st;
+        if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, true, &fz, nullptr))) return st;
         return dev(ql::launch_fused_grads_finalize(pl, ws, d_lora_a, d_lora_b, s, f16));
     }
-    if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, r > 0, nullptr, dx_add))) return st;
+    if (int st = dev(ql::launch_dx(dy, codes, sc, lora_a, pl, ws, dx, s, f16, r > 0, nullptr, nullptr))) return st;
     if (grads) {
         if (!reuse)
             if (int st = recompute_p()) return st;
-        if (int st = dev(ql::launch_lora_grads(x, dy, pl, ws, d_lora_a, d_lora_b, s, f16))) return st;
+        if (int st = dev(ql::launch_lora_grads(ql::Saved{x, nullptr, nullptr}, dy, pl, ws, d_lora_a, d_lora_b, s, f16))) return st;
     }
     return QLORA_OK;
 }
@@ -226,7 +229,7 @@ int bwd_impl(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint8_t*
     const bool reuse = (flags & QLORA_BWD_REUSE_FORWARD) && T > ql::kChunkMaxT;
     if (need && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
 
-    return bwd_launch(dy, codes, sc, lora_a, lora_b, scaling, dx, nullptr, x, d_lora_a, d_lora_b, pl,
+    return bwd_launch(dy, codes, sc, lora_a, lora_b, scaling, dx, x, d_lora_a, d_lora_b, pl,
                       static_cast<uint8_t*>(workspace), reuse, fused, static_cast<hipStream_t>(stream), f16);
 }
 
@@ -341,15 +344,16 @@ int act_fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8
 }
 
 // Workspace of the backward from saved activations: the layer backward's own
-// regions, then dZ, X in 16 bits and the column-sum partials of the bias gradient.
+// regions, then dZ, the split partials of s X A (which run beside those of
+// s dZ B^T) and the column-sum partials of the bias gradient.
 struct ActBwdPlan {
     ql::LoraPlan pl;
-    size_t off_dz, off_x, off_part, bytes;
+    size_t off_dz, off_xpart, off_part, bytes;
     ActBwdPlan(int64_t T, int64_t K, int64_t N, int64_t r) : pl(T, K, N, r) {
         size_t o = ql::align256(std::max(pl.bwd_grad_bytes, pl.bwd_bytes));
-        off_dz = o;   o = ql::align256(o + (size_t)T * N * 2);
-        off_x = o;    o = ql::align256(o + (r > 0 ? (size_t)T * K * 2 : 0));
-        off_part = o; o = ql::align256(o + (size_t)ql::act_bwd_ranges(T) * N * 4);
+        off_dz = o;    o = ql::align256(o + (size_t)T * N * 2);
+        off_xpart = o; o = ql::align256(o + (pl.s_down_x > 1 ? (size_t)pl.s_down_x * T * pl.r_pad * 4 : 0));
+        off_part = o;  o = ql::align256(o + (size_t)ql::act_bwd_ranges(T, N) * N * 4);
         bytes = o;
     }
 };
@@ -385,24 +389,33 @@ int act_bwd_impl(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const uint16_t* dz = dy;                                           // without act and mul, dZ is dY itself
+    const ql::LoraPlan& pl = ap.pl;
+    // 1: dZ, dmul and the column sums; the transposed block scales of dX and A^T
+    // of s X A ride along.  Without act and mul, dZ is dY itself.
     const bool own_dz = g->act != QLORA_ACT_NONE || sm.present();
-    if (own_dz || g->d_bias) {
-        uint16_t* out = own_dz ? reinterpret_cast<uint16_t*>(ws + ap.off_dz) : nullptr;
-        const ql::ActBwd a{g->act, dy, sz, sm, out, g->d_mul,
-                           g->d_bias ? reinterpret_cast<float*>(ws + ap.off_part) : nullptr, T, N,
-                           ql::act_bwd_rows(T)};
-        if (int st = dev(ql::launch_act_bwd(a, g->d_bias, s, f16))) return st;
-        if (own_dz) dz = out;
+    uint16_t* const dz_ws = reinterpret_cast<uint16_t*>(ws + ap.off_dz);
+    float* const part = reinterpret_cast<float*>(ws + ap.off_part);
+    const int64_t ranges = ql::act_bwd_ranges(T, N);
+    const ql::ActBwd a{g->act, dy, sz, sm, own_dz ? dz_ws : nullptr, g->d_mul, g->d_bias ? part : nullptr, T, N,
+                       ql::act_bwd_rows(T, N),
+                       own_dz || g->d_bias ? (int)(ql::ceil_div(N, 128) * ranges) : 0};
+    const ql::TransposeJob tj = grads ? ql::transpose_job_for(lora_a, pl, ws) : ql::TransposeJob{};
+    if (int st = dev(ql::launch_act_bwd(a, ql::scales_job_for(sc, pl, ws), tj, s, f16))) return st;
+    const uint16_t* dz = own_dz ? dz_ws : dy;
+    // 2: s dZ B^T and s X A, and the bias gradient
+    const ql::BiasFin bf{part, ranges, N, g->d_bias};
+    if (r > 0) {
+        const ql::Saved x = grads ? sx : ql::Saved{};
+        if (int st = dev(ql::launch_lora_down_pair(dz, lora_b, x, scaling, pl, ws,
+                                                   reinterpret_cast<float*>(ws + ap.off_xpart), bf, s, f16)))
+            return st;
+    } else if (g->d_bias) {
+        if (int st = dev(ql::launch_bias_fin(bf, s, f16))) return st;
     }
-    const uint16_t* x = sx.v;
-    if (grads && sx.codes) {
-        uint16_t* x16 = reinterpret_cast<uint16_t*>(ws + ap.off_x);
-        if (int st = dev(ql::launch_act8_dequantize(sx.codes, sx.scale, T * K, x16, s, f16))) return st;
-        x = x16;
-    }
-    return bwd_launch(dz, codes, sc, lora_a, lora_b, scaling, g->dx, g->dx_add, x, g->d_lora_a, g->d_lora_b, ap.pl,
-                      ws, false, false, s, f16);
+    // 3: the gradients
+    if (int st = dev(ql::launch_dx(dz, codes, sc, lora_a, pl, ws, g->dx, s, f16, true, nullptr, g->dx_add))) return st;
+    if (!grads) return QLORA_OK;
+    return dev(ql::launch_lora_grads(sx, dz, pl, ws, g->d_lora_a, g->d_lora_b, s, f16));
 }
 
 // ------------------------------------------------------------ no-allocation forward

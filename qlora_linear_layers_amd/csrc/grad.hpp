@@ -15,12 +15,17 @@
 // fixed order, so the result is deterministic.
 #pragma once
 
+#include <type_traits>
+
+#include "act.hpp"
 #include "common.hpp"
 
 namespace ql {
 
 struct GradArgs {
     const uint16_t* s;       // [T][C] bf16 (X or dY)
+    const int8_t* sc;        // or its 8-bit checkpoint: codes [T][C] and
+    const float* sd;         // scales [T][C / 64]
     const uint16_t* vt_hi;   // [r_pad][ldt] bf16 (G^T or P^T, hi and lo; tokens [0, T8))
     const uint16_t* vt_lo;
     float* part;             // [splits][C][r_pad] fp32
@@ -50,15 +55,17 @@ constexpr size_t kGradSmem = (size_t)4 * 8 * 4 * 64 * 4 * 4;   // the wave sums,
 // columns of block cb and the ranks j0 .. j0 + 63 (lane l: operand i is
 // column cb 128 + 8 (l % 16) + i; acc[i][jt][v] is column
 // cb 128 + 8 (4 (l / 16) + v) + i, rank j0 + 16 jt + l % 16).  The chunks are
-// walked from chunk `rot` on, in a fixed order.
-template <bool F16>
+// walked from chunk `rot` on, in a fixed order.  Q8: S is an 8-bit checkpoint;
+// a lane loads the eight codes and the scale of each of its eight tokens.
+template <bool F16, bool Q8 = false>
 QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int rot, int64_t j0,
                             f32x4_t (&acc)[8][4]) {
     const int l = threadIdx.x & 63;
     const int64_t c0 = (int64_t)cb * 128 + 8 * (l & 15);          // this lane's 8 columns
     const int tl8 = 8 * (l >> 4);                                 // lane's token group in a chunk
 
-    const rsrc_t rs = make_rsrc(a.s, a.T * a.C * 2);
+    const rsrc_t rs = Q8 ? make_rsrc(a.sc, a.T * a.C) : make_rsrc(a.s, a.T * a.C * 2);
+    [[maybe_unused]] const rsrc_t rd = make_rsrc(a.sd, Q8 ? a.T * a.C / 16 : 0);
     const rsrc_t rh = make_rsrc(a.vt_hi, a.r_pad * a.ldt * 2);
     const rsrc_t rl = make_rsrc(a.vt_lo, a.r_pad * a.ldt * 2);
     const bool cok = c0 < a.C;
@@ -68,7 +75,10 @@ QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int 
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) acc[i][jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-    u32x4_t xr[2][8], vh[2][4], vl[2][4];
+    using xreg_t = std::conditional_t<Q8, u32x2_t, u32x4_t>;
+    xreg_t xr[2][8];
+    [[maybe_unused]] uint32_t dr[2][8];
+    u32x4_t vh[2][4], vl[2][4];
     auto load = [&](int ch, int slot) {
         const bool live = ch < nch;
         int cr = live ? ch + rot : 0;
@@ -77,7 +87,13 @@ QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int 
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             const int64_t t = tc + s;
-            xr[slot][s] = bload16(rs, (live && cok && t < a.T) ? (uint32_t)((t * a.C + c0) * 2) : kOOB, 0);
+            const bool ok = live && cok && t < a.T;
+            if constexpr (Q8) {
+                xr[slot][s] = bload8(rs, ok ? (uint32_t)(t * a.C + c0) : kOOB, 0);
+                dr[slot][s] = bload4(rd, ok ? (uint32_t)((t * a.C + c0) / 64 * 4) : kOOB, 0);
+            } else {
+                xr[slot][s] = bload16(rs, ok ? (uint32_t)((t * a.C + c0) * 2) : kOOB, 0);
+            }
         }
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) {
@@ -88,6 +104,12 @@ QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int 
         }
     };
     auto compute = [&](int slot) {
+        u32x4_t xv[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if constexpr (Q8) xv[s] = ck_pack8<F16>(xr[slot][s], __uint_as_float(dr[slot][s]));
+            else xv[s] = xr[slot][s];
+        }
         // transpose the 8 x 8 block: operand i holds column c0 + i over the 8 tokens
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -95,7 +117,7 @@ QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int 
             u32x4_t o;
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                o[p] = __builtin_amdgcn_perm(xr[slot][2 * p + 1][i >> 1], xr[slot][2 * p][i >> 1], sel);
+                o[p] = __builtin_amdgcn_perm(xv[2 * p + 1][i >> 1], xv[2 * p][i >> 1], sel);
             const bf16x8_t xi = __builtin_bit_cast(bf16x8_t, o);
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
@@ -119,13 +141,13 @@ QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int 
 // from (4 split + w) 32 cpw).  Every thread of a 256-thread workgroup calls
 // it with the same arguments; `red` is kGradSmem bytes of LDS.  It ends with
 // a barrier, so calls can follow one another on the same LDS.
-template <bool F16>
+template <bool F16, bool Q8 = false>
 QL_DEV void grad_block(const GradArgs& a, int cb, int split, int64_t j0, float* red) {
     const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
     f32x4_t acc[8][4];
     // workgroups of one split read the same V columns; each column block walks
     // its chunks from its own starting point
-    grad_accumulate<F16>(a, cb, ((int64_t)split * 4 + w) * 32 * a.cpw, a.cpw, (int)(cb % a.cpw), j0, acc);
+    grad_accumulate<F16, Q8>(a, cb, ((int64_t)split * 4 + w) * 32 * a.cpw, a.cpw, (int)(cb % a.cpw), j0, acc);
 
     // fixed-order sum of the four waves, then one fp32 partial per split
 #pragma unroll

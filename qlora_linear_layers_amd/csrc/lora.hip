@@ -23,6 +23,9 @@
 // 64-rank block per workgroup; token ranges of different workgroups produce
 // fp32 partials that k_grad_finalize sums in split order.  Every result is
 // deterministic.
+#include <type_traits>
+
+#include "act.hpp"
 #include "common.hpp"
 #include "grad.hpp"
 #include "plan.hpp"
@@ -52,40 +55,18 @@ QL_DEV void split_hi_lo(float v, uint16_t& hi, uint16_t& lo) {
 
 // ------------------------------------------------------------------ transpose
 
-// dst[j][k] (row stride ldd) = src[k][j] for j < r, 0 for r <= j < r_pad
-// (src [K][r] bf16, r a multiple of 8).  One workgroup per 64 k x 64 j tile:
-// 16-byte loads of 8 j, an LDS tile, 16-byte stores of 8 k.
-__global__ __launch_bounds__(kThreads) void k_transpose(const uint16_t* __restrict__ src, int64_t K, int64_t r,
-                                                        int64_t r_pad, int64_t ldd, uint16_t* __restrict__ dst) {
-    __shared__ uint16_t tile[64][64 + 8];
-    const int64_t k0 = (int64_t)blockIdx.x * 64, j0 = (int64_t)blockIdx.y * 64;
-    const int row = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;     // 32 rows x 8 chunks per pass
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int kk = row + 32 * h;
-        const int64_t k = k0 + kk, j = j0 + c8;
-        u32x4_t v = {0, 0, 0, 0};
-        if (k < K && j < r) v = *reinterpret_cast<const u32x4_t*>(src + k * r + j);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tile[kk][c8 + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int jj = row + 32 * h;
-        const int64_t j = j0 + jj, k = k0 + c8;
-        if (j >= r_pad || k >= K) continue;
-        u32x4_t v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (uint32_t)tile[c8 + 2 * e][jj] | ((uint32_t)tile[c8 + 2 * e + 1][jj] << 16);
-        *reinterpret_cast<u32x4_t*>(dst + j * ldd + k) = v;
-    }
+// One workgroup per 64 k x 64 j tile (see TransposeJob).
+__global__ __launch_bounds__(kThreads) void k_transpose(TransposeJob j) {
+    __shared__ __align__(16) uint8_t lds[kTransposeLds];
+    transpose_job(j, (int)blockIdx.x, (lds8_t*)lds);
 }
 
 // ------------------------------------------------------------------ down projections
 
 struct DownArgs {
     const uint16_t* s;    // [T][L] bf16 (X or dY)
+    const int8_t* sc;     // or its 8-bit checkpoint: codes [T][L] and
+    const float* sd;      // scales [T][L / 64]
     const uint16_t* m;    // [m_rows][ldm] bf16 (A^T or B); rows m_rows .. r_pad-1 read as zero
     int64_t T, L, ldm, m_rows, r_pad;
     float scale;
@@ -137,21 +118,19 @@ QL_DEV void down_emit(const DownArgs& a, const float* sum, int64_t t0) {
 // fragments, so every global load fetches whole cache lines and M is read
 // once per 64 rows.  With several splits each workgroup stores an fp32
 // partial (whole rows, through LDS) and k_down_fin adds them in split order.
-template <int RT, bool F16>
-__global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
+//
+// Q8: S is an 8-bit checkpoint.  A round is one block of 64 codes per row, so a
+// thread loads the eight codes of its 16-byte chunk and the row's scale, and
+// rounds the eight values q d to 16 bits on their way to LDS.
+template <int RT, bool F16, bool Q8>
+QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     constexpr int PD = RT <= 4 ? 4 : 2;
     constexpr int NX = 2;            // 16-byte chunks of the 64 x 64 S tile per thread
     constexpr int NM = RT / 2;       // 16-byte chunks of the r_pad x 64 M tile per thread
     constexpr int R = RT * 16;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
     lds8_t* smem = (lds8_t*)(smem_raw);
     constexpr uint32_t kXT = 64 * 128, kMT = R * 128, kBuf = kXT + kMT;
     const int tiles = (int)ceil_div(a.T, 64);
-    const int bid = (int)blockIdx.x;
-    if (bid >= tiles * a.splits) {              // block-scale workgroups of the same launch, dispatched
-        scales_job(a.sj, bid - tiles * a.splits, smem);   // after the longer projection workgroups
-        return;
-    }
     const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int tile = bid % tiles, split = bid / tiles;
     const int64_t t0 = (int64_t)tile * 64;
@@ -159,14 +138,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
     const int r0 = split * nr_all / a.splits, r1 = (split + 1) * nr_all / a.splits;
     const int nr = r1 - r0;
 
-    const rsrc_t rx = make_rsrc(a.s, a.T * a.L * 2);
+    const rsrc_t rx = Q8 ? make_rsrc(a.sc, a.T * a.L) : make_rsrc(a.s, a.T * a.L * 2);
+    [[maybe_unused]] const rsrc_t rd = make_rsrc(a.sd, Q8 ? a.T * a.L / 16 : 0);
     const rsrc_t rm = make_rsrc(a.m, a.m_rows * a.ldm * 2);
     uint32_t xo[NX], mo[NM];
+    [[maybe_unused]] uint32_t dof[NX];
 #pragma unroll
     for (int u = 0; u < NX; ++u) {
         const int q = threadIdx.x + u * kThreads;
         const int64_t t = t0 + (q >> 3);
-        xo[u] = t < a.T ? (uint32_t)((t * a.L + (int64_t)r0 * 64 + (q & 7) * 8) * 2) : kOOB;
+        xo[u] = t < a.T ? (uint32_t)((t * a.L + (int64_t)r0 * 64 + (q & 7) * 8) * (Q8 ? 1 : 2)) : kOOB;
+        if constexpr (Q8) dof[u] = t < a.T ? (uint32_t)((t * (a.L / 64) + r0) * 4) : kOOB;
     }
 #pragma unroll
     for (int u = 0; u < NM; ++u) {
@@ -174,12 +156,22 @@ __global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
         const int64_t j = q >> 3;
         mo[u] = j < a.m_rows ? (uint32_t)((j * a.ldm + (int64_t)r0 * 64 + (q & 7) * 8) * 2) : kOOB;
     }
-    u32x4_t xr[PD][NX], mr[PD][NM];
+    using xreg_t = std::conditional_t<Q8, u32x2_t, u32x4_t>;
+    xreg_t xr[PD][NX];
+    [[maybe_unused]] uint32_t dr[PD][NX];
+    u32x4_t mr[PD][NM];
     auto load = [&](int i, int slot) {           // round i of this split (zeros past nr)
         const bool ok = i < nr;
         const uint32_t so = ok ? (uint32_t)i * 128u : 0u;
 #pragma unroll
-        for (int u = 0; u < NX; ++u) xr[slot][u] = bload16(rx, ok ? xo[u] : kOOB, so);
+        for (int u = 0; u < NX; ++u) {
+            if constexpr (Q8) {
+                xr[slot][u] = bload8(rx, ok ? xo[u] : kOOB, so >> 1);
+                dr[slot][u] = bload4(rd, ok ? dof[u] : kOOB, so >> 5);
+            } else {
+                xr[slot][u] = bload16(rx, ok ? xo[u] : kOOB, so);
+            }
+        }
 #pragma unroll
         for (int u = 0; u < NM; ++u) mr[slot][u] = bload16(rm, ok ? mo[u] : kOOB, so);
     };
@@ -187,7 +179,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
 #pragma unroll
         for (int u = 0; u < NX; ++u) {
             const int q = threadIdx.x + u * kThreads;
-            *reinterpret_cast<lds_u32x4_t*>(buf + lds_off(q >> 3, q & 7)) = xr[slot][u];
+            u32x4_t v;
+            if constexpr (Q8) v = ck_pack8<F16>(xr[slot][u], __uint_as_float(dr[slot][u]));
+            else v = xr[slot][u];
+            *reinterpret_cast<lds_u32x4_t*>(buf + lds_off(q >> 3, q & 7)) = v;
         }
 #pragma unroll
         for (int u = 0; u < NM; ++u) {
@@ -249,13 +244,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
     }
 }
 
+template <int RT, bool F16>
+__global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const int n = (int)ceil_div(a.T, 64) * a.splits, bid = (int)blockIdx.x;
+    if (bid >= n) {                             // block-scale workgroups of the same launch, dispatched
+        scales_job(a.sj, bid - n, (lds8_t*)smem_raw);     // after the longer projection workgroups
+        return;
+    }
+    down_block<RT, F16, false>(a, bid, smem_raw);
+}
+
+// Both down projections of a backward in one launch, then the sums of the bias
+// gradient: workgroups [0, n0) take a0 (s dZ B^T), [n0, n0 + n1) a1 (s X A, X a
+// checkpoint when Q8), the rest 256 columns of the bias gradient each.
+template <int RT, bool F16, bool Q8>
+__global__ __launch_bounds__(kThreads, 2) void k_down2(DownArgs a0, DownArgs a1, int n0, int n1, BiasFin bf) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const int bid = (int)blockIdx.x;
+    if (bid < n0) down_block<RT, F16, false>(a0, bid, smem_raw);
+    else if (bid < n0 + n1) down_block<RT, F16, Q8>(a1, bid - n0, smem_raw);
+    else bias_fin<F16>(bf, bid - n0 - n1);
+}
+
 // Split-ordered sum of the k_down partials of 16 rows, then both layouts.
 template <int RT, bool F16>
-__global__ __launch_bounds__(kThreads) void k_down_fin(DownArgs a) {
+QL_DEV void down_fin_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     constexpr int R = RT * 16;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
     float* sum = reinterpret_cast<float*>(smem_raw);           // [16][R + 4]
-    const int64_t t0 = (int64_t)blockIdx.x * 16;
+    const int64_t t0 = (int64_t)bid * 16;
     for (int e = threadIdx.x; e < 4 * R; e += kThreads) {
         const int tl = e / (R / 4), j = 4 * (e % (R / 4));
         const int64_t t = t0 + tl;
@@ -275,18 +292,34 @@ __global__ __launch_bounds__(kThreads) void k_down_fin(DownArgs a) {
     down_emit<R, 16, F16>(a, sum, t0);
 }
 
+// workgroups [0, n0) take a0, the rest a1 (n0 workgroups alone for one problem)
+template <int RT, bool F16>
+__global__ __launch_bounds__(kThreads) void k_down_fin(DownArgs a0, DownArgs a1, int n0) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const int bid = (int)blockIdx.x;
+    if (bid < n0) down_fin_block<RT, F16>(a0, bid, smem_raw);
+    else down_fin_block<RT, F16>(a1, bid - n0, smem_raw);
+}
+
 // ------------------------------------------------------------------ adapter gradients
 
 // One launch serves both adapter gradients: workgroups [0, blocks0) take
 // problem a0 (dA = X^T G), the rest problem a1 (dB = P^T dY); blockIdx.y
-// picks the 64 ranks.
-template <bool F16>
+// picks the 64 ranks.  Q8: a0's X is an 8-bit checkpoint.
+template <bool F16, bool Q8>
 __global__ __launch_bounds__(kThreads, 1) void k_grad(GradArgs a0, GradArgs a1, int blocks0) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const bool second = (int)blockIdx.x >= blocks0;
     const GradArgs& a = second ? a1 : a0;
     const int bx = second ? (int)blockIdx.x - blocks0 : (int)blockIdx.x;
-    grad_block<F16>(a, bx % a.cblocks, bx / a.cblocks, (int64_t)blockIdx.y * 64, reinterpret_cast<float*>(smem_raw));
+    float* red = reinterpret_cast<float*>(smem_raw);
+    if constexpr (Q8) {
+        if (!second) {
+            grad_block<F16, true>(a0, bx % a0.cblocks, bx / a0.cblocks, (int64_t)blockIdx.y * 64, red);
+            return;
+        }
+    }
+    grad_block<F16, false>(a, bx % a.cblocks, bx / a.cblocks, (int64_t)blockIdx.y * 64, red);
 }
 
 // dA[k][j] (transpose = 0) or dB[j][n] (transpose = 1): RNE_bf16 of the
@@ -370,9 +403,45 @@ hipError_t down_rt(const DownArgs& a, hipStream_t s) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         const size_t fl = (size_t)16 * (R + 4) * 4;
-        hipLaunchKernelGGL((k_down_fin<RT, F16>), dim3((unsigned)ceil_div(a.T, 16)), dim3(kThreads), fl, s, a);
+        const int n = (int)ceil_div(a.T, 16);
+        hipLaunchKernelGGL((k_down_fin<RT, F16>), dim3((unsigned)n), dim3(kThreads), fl, s, a, a, n);
     }
     return hipGetLastError();
+}
+
+// a0 and (when `second`) a1 in one k_down2 launch, the split sums of both in one more
+template <int RT, bool F16>
+hipError_t down2_rt(const DownArgs& a0, const DownArgs& a1, bool second, const BiasFin& bf, hipStream_t s) {
+    constexpr int R = RT * 16;
+    const size_t bufs = (size_t)2 * (64 + R) * 128, sums = (size_t)64 * (R + 4) * 4;
+    const size_t lds = bufs > sums ? bufs : sums;
+    const int tiles = (int)ceil_div(a0.T, 64), n0 = tiles * a0.splits, n1 = second ? tiles * a1.splits : 0;
+    auto go = [&](auto kern) {
+        hipError_t e = set_smem(kern, lds);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kern, dim3((unsigned)(n0 + n1 + bias_fin_blocks(bf))), dim3(kThreads), lds, s, a0, a1, n0,
+                           n1, bf);
+        return hipGetLastError();
+    };
+    hipError_t e = a1.sc ? go(k_down2<RT, F16, true>) : go(k_down2<RT, F16, false>);
+    if (e != hipSuccess) return e;
+    const int f = (int)ceil_div(a0.T, 16), f0 = a0.splits > 1 ? f : 0, f1 = second && a1.splits > 1 ? f : 0;
+    if (f0 + f1 > 0) {
+        const size_t fl = (size_t)16 * (R + 4) * 4;
+        hipLaunchKernelGGL((k_down_fin<RT, F16>), dim3((unsigned)(f0 + f1)), dim3(kThreads), fl, s, a0, a1, f0);
+    }
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t down2_t(const DownArgs& a0, const DownArgs& a1, bool second, const BiasFin& bf, hipStream_t s) {
+    switch (a0.r_pad / 16) {
+        case 4: return down2_rt<4, F16>(a0, a1, second, bf, s);
+        case 8: return down2_rt<8, F16>(a0, a1, second, bf, s);
+        case 12: return down2_rt<12, F16>(a0, a1, second, bf, s);
+        case 16: return down2_rt<16, F16>(a0, a1, second, bf, s);
+        default: return hipErrorInvalidValue;
+    }
 }
 
 template <bool F16>
@@ -397,7 +466,8 @@ hipError_t grad(const GradArgs& a0, int n0, const GradArgs& a1, int n1, int64_t 
                            a0, a1, n0);
         return hipGetLastError();
     };
-    return f16 ? go(k_grad<true>) : go(k_grad<false>);
+    if (a0.sc) return f16 ? go(k_grad<true, true>) : go(k_grad<false, true>);
+    return f16 ? go(k_grad<true, false>) : go(k_grad<false, false>);
 }
 
 // One k_grad_finalize launch for dA (fa, when has_a) and dB (fb, when has_b).
@@ -417,49 +487,79 @@ hipError_t grad_finalize(GradFin fa, bool has_a, const GradFin& fb, bool has_b, 
 
 }  // namespace
 
+TransposeJob transpose_job_for(const uint16_t* lora_a, const LoraPlan& pl, uint8_t* ws) {
+    return TransposeJob{lora_a, pl.K, pl.r, pl.r_pad, pl.ld_at, reinterpret_cast<uint16_t*>(ws + pl.off_at),
+                        (int)(ceil_div(pl.K, 64) * (pl.r_pad / 64))};
+}
+
 hipError_t launch_transpose_a(const uint16_t* lora_a, const LoraPlan& pl, uint8_t* ws, hipStream_t s) {
-    uint16_t* at = reinterpret_cast<uint16_t*>(ws + pl.off_at);
-    hipLaunchKernelGGL(k_transpose, dim3((unsigned)ceil_div(pl.K, 64), (unsigned)(pl.r_pad / 64)), dim3(kThreads),
-                       0, s, lora_a, pl.K, pl.r, pl.r_pad, pl.ld_at, at);
+    const TransposeJob j = transpose_job_for(lora_a, pl, ws);
+    hipLaunchKernelGGL(k_transpose, dim3((unsigned)j.blocks), dim3(kThreads), 0, s, j);
     return hipGetLastError();
 }
 
+namespace {
+
 // s X A -> P (hi/lo [T][r_pad]; also transposed when `transposed`).  Needs A^T in ws.
+DownArgs down_x_args(const Saved& x, float scaling, const LoraPlan& pl, uint8_t* ws, bool transposed) {
+    return DownArgs{x.v, x.codes, x.scale, reinterpret_cast<const uint16_t*>(ws + pl.off_at), pl.T, pl.K, pl.ld_at,
+                    pl.r_pad, pl.r_pad, scaling,
+                    reinterpret_cast<uint16_t*>(ws + pl.off_ps_hi), reinterpret_cast<uint16_t*>(ws + pl.off_ps_lo),
+                    transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_pst_hi) : nullptr,
+                    transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_pst_lo) : nullptr, pl.T8, pl.ld_t,
+                    reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_x, ScalesJob{}};
+}
+
+// s dY B^T -> G (hi/lo [T][r_pad], also transposed when `transposed`)
+DownArgs down_dy_args(const uint16_t* dy, const uint16_t* lora_b, float scaling, const LoraPlan& pl, uint8_t* ws,
+                      bool transposed) {
+    return DownArgs{dy, nullptr, nullptr, lora_b, pl.T, pl.N, pl.N, pl.r, pl.r_pad, scaling,
+                    reinterpret_cast<uint16_t*>(ws + pl.off_gs_hi), reinterpret_cast<uint16_t*>(ws + pl.off_gs_lo),
+                    transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_gst_hi) : nullptr,
+                    transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_gst_lo) : nullptr, pl.T8, pl.ld_t,
+                    reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_dy, ScalesJob{}};
+}
+
+}  // namespace
+
 hipError_t launch_lora_down_x(const uint16_t* x, float scaling, const LoraPlan& pl, uint8_t* ws, bool transposed,
                               hipStream_t s, bool f16) {
-    DownArgs a{x, reinterpret_cast<const uint16_t*>(ws + pl.off_at), pl.T, pl.K, pl.ld_at, pl.r_pad, pl.r_pad,
-               scaling,
-               reinterpret_cast<uint16_t*>(ws + pl.off_ps_hi), reinterpret_cast<uint16_t*>(ws + pl.off_ps_lo),
-               transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_pst_hi) : nullptr,
-               transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_pst_lo) : nullptr, pl.T8, pl.ld_t,
-               reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_x, ScalesJob{}};
+    return down(down_x_args(Saved{x, nullptr, nullptr}, scaling, pl, ws, transposed), s, f16);
+}
+
+// `scales` (if not NULL) runs as extra workgroups of the same launch.
+hipError_t launch_lora_down_dy(const uint16_t* dy, const uint16_t* lora_b, float scaling, const LoraPlan& pl,
+                               uint8_t* ws, bool transposed, hipStream_t s, bool f16, const ScalesJob* scales) {
+    DownArgs a = down_dy_args(dy, lora_b, scaling, pl, ws, transposed);
+    if (scales) a.sj = *scales;
     return down(a, s, f16);
 }
 
-// s dY B^T -> G (hi/lo [T][r_pad] and transposed); `scales` (if not NULL) runs
-// as extra workgroups of the same launch.
-hipError_t launch_lora_down_dy(const uint16_t* dy, const uint16_t* lora_b, float scaling, const LoraPlan& pl,
-                               uint8_t* ws, bool transposed, hipStream_t s, bool f16, const ScalesJob* scales) {
-    DownArgs a{dy, lora_b, pl.T, pl.N, pl.N, pl.r, pl.r_pad, scaling,
-               reinterpret_cast<uint16_t*>(ws + pl.off_gs_hi), reinterpret_cast<uint16_t*>(ws + pl.off_gs_lo),
-               transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_gst_hi) : nullptr,
-               transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_gst_lo) : nullptr, pl.T8, pl.ld_t,
-               reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_dy, scales ? *scales : ScalesJob{}};
-    return down(a, s, f16);
+// G and, with `x` present, P (needs A^T in ws), both transposed too then; and
+// the bias gradient.  The two projections' split partials need room of their
+// own: P's follow G's at `xpart`.
+hipError_t launch_lora_down_pair(const uint16_t* dz, const uint16_t* lora_b, const Saved& x, float scaling,
+                                 const LoraPlan& pl, uint8_t* ws, float* xpart, const BiasFin& bf, hipStream_t s,
+                                 bool f16) {
+    const bool second = x.present();
+    const DownArgs a0 = down_dy_args(dz, lora_b, scaling, pl, ws, second);
+    DownArgs a1 = down_x_args(x, scaling, pl, ws, true);
+    a1.part = xpart;
+    return f16 ? down2_t<true>(a0, a1, second, bf, s) : down2_t<false>(a0, a1, second, bf, s);
 }
 
 // dA = X^T G and dB = P^T dY from the transposed intermediates in ws.
-hipError_t launch_lora_grads(const uint16_t* x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws,
+hipError_t launch_lora_grads(const Saved& x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws,
                              uint16_t* d_lora_a, uint16_t* d_lora_b, hipStream_t s, bool f16) {
     float* pda = reinterpret_cast<float*>(ws + pl.off_pda);
     float* pdb = reinterpret_cast<float*>(ws + pl.off_pdb);
     GradFin fa{pda, pl.s_da, pl.K, pl.r_pad, pl.r, d_lora_a, 0};
     GradFin fb{pdb, pl.s_db, pl.N, pl.r_pad, pl.r, d_lora_b, 1};
     // dA and dB in one launch (either may be absent)
-    const GradArgs ga{x, reinterpret_cast<const uint16_t*>(ws + pl.off_gst_hi),
+    const GradArgs ga{x.v, x.codes, x.scale, reinterpret_cast<const uint16_t*>(ws + pl.off_gst_hi),
                       reinterpret_cast<const uint16_t*>(ws + pl.off_gst_lo), pda, pl.T, pl.T8, pl.ld_t, pl.K,
                       pl.r_pad, (int)ceil_div(pl.K, 128), pl.cpw_da};
-    const GradArgs gb{dy, reinterpret_cast<const uint16_t*>(ws + pl.off_pst_hi),
+    const GradArgs gb{dy, nullptr, nullptr, reinterpret_cast<const uint16_t*>(ws + pl.off_pst_hi),
                       reinterpret_cast<const uint16_t*>(ws + pl.off_pst_lo), pdb, pl.T, pl.T8, pl.ld_t, pl.N,
                       pl.r_pad, (int)ceil_div(pl.N, 128), pl.cpw_db};
     const int na = d_lora_a ? ga.cblocks * pl.s_da : 0, nb = d_lora_b ? gb.cblocks * pl.s_db : 0;
@@ -480,11 +580,11 @@ FusedGrads fused_grads_for(const uint16_t* x, const uint16_t* dy, const LoraPlan
     f.groups = pl.s_fz;
     f.waves = 0;                                   // set by the dX launcher from its grid
     if (da)
-        f.ga = GradArgs{x, reinterpret_cast<const uint16_t*>(ws + pl.off_gst_hi),
+        f.ga = GradArgs{x, nullptr, nullptr, reinterpret_cast<const uint16_t*>(ws + pl.off_gst_hi),
                         reinterpret_cast<const uint16_t*>(ws + pl.off_gst_lo), reinterpret_cast<float*>(ws + pl.off_fza),
                         pl.T, pl.T8, pl.ld_t, pl.K, pl.r_pad, (int)ceil_div(pl.K, 128), 8};
     if (db)
-        f.gb = GradArgs{dy, reinterpret_cast<const uint16_t*>(ws + pl.off_pst_hi),
+        f.gb = GradArgs{dy, nullptr, nullptr, reinterpret_cast<const uint16_t*>(ws + pl.off_pst_hi),
                         reinterpret_cast<const uint16_t*>(ws + pl.off_pst_lo), reinterpret_cast<float*>(ws + pl.off_fzb),
                         pl.T, pl.T8, pl.ld_t, pl.N, pl.r_pad, (int)ceil_div(pl.N, 128), 8};
     return f;
