@@ -206,16 +206,15 @@ QL_DEV void act_bwd_block(const ActBwd& a, int bid, float* red) {
     }
 }
 
-constexpr int kActBwdLds = kTransposeLds > 16 * 132 * 4 ? kTransposeLds : 16 * 132 * 4;
-static_assert(kScalesLds <= kActBwdLds, "the jobs share the workgroup's LDS");
+constexpr int kActBwdLds = 16 * 132 * 4;
+static_assert(kScalesLds <= kActBwdLds, "the job shares the workgroup's LDS");
 
 template <int ACT, bool F16>
-__global__ __launch_bounds__(kThreads) void k_act_bwd(ActBwd a, ScalesJob sj, TransposeJob tj) {
+__global__ __launch_bounds__(kThreads) void k_act_bwd(ActBwd a, ScalesJob sj) {
     __shared__ __align__(16) uint8_t lds[kActBwdLds];
     const int bid = (int)blockIdx.x;
     if (bid < a.blocks) act_bwd_block<ACT, F16>(a, bid, reinterpret_cast<float*>(lds));
-    else if (bid < a.blocks + sj.blocks) scales_job(sj, bid - a.blocks, (lds8_t*)lds);
-    else transpose_job(tj, bid - a.blocks - sj.blocks, (lds8_t*)lds);
+    else scales_job(sj, bid - a.blocks, (lds8_t*)lds);
 }
 
 template <bool F16>
@@ -241,10 +240,10 @@ hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64
     return hipGetLastError();
 }
 
-hipError_t launch_act_bwd(const ActBwd& a, const ScalesJob& sj, const TransposeJob& tj, hipStream_t s, bool f16) {
-    const int n = a.blocks + sj.blocks + tj.blocks;
+hipError_t launch_act_bwd(const ActBwd& a, const ScalesJob& sj, hipStream_t s, bool f16) {
+    const int n = a.blocks + sj.blocks;
     if (n == 0) return hipSuccess;
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(kThreads), 0, s, a, sj, tj); };
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(kThreads), 0, s, a, sj); };
     switch (a.act) {
         case kActRelu: f16 ? go(k_act_bwd<kActRelu, true>) : go(k_act_bwd<kActRelu, false>); break;
         case kActSilu: f16 ? go(k_act_bwd<kActSilu, true>) : go(k_act_bwd<kActSilu, false>); break;

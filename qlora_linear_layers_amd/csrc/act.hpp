@@ -275,19 +275,13 @@ struct ActBwd {
     int blocks;               // workgroups of the elementwise pass, 0 = none
 };
 
-// Rows of one range: enough workgroups (128 columns each) for four a CU, at
-// most 64 ranges with a bias gradient (its partials are summed range by range).
+// Rows of one range: 64, or more where that would be over 64 ranges (the
+// partials of the bias gradient are summed range by range).
 constexpr int64_t kActBwdMaxRanges = 64;
-inline int64_t act_bwd_rows(int64_t T, int64_t N) {
-    const int64_t cb = (N + 127) / 128;
-    int64_t r = T * cb / 1024 / 64 * 64;
-    if (r < 64) r = 64;
-    const int64_t least = ((T + kActBwdMaxRanges - 1) / kActBwdMaxRanges + 63) / 64 * 64;
-    return r > least ? r : least;
+inline int64_t act_bwd_rows(int64_t T) {
+    return ((T + kActBwdMaxRanges - 1) / kActBwdMaxRanges + 63) / 64 * 64;
 }
-inline int64_t act_bwd_ranges(int64_t T, int64_t N) {
-    return (T + act_bwd_rows(T, N) - 1) / act_bwd_rows(T, N);
-}
+inline int64_t act_bwd_ranges(int64_t T) { return (T + act_bwd_rows(T) - 1) / act_bwd_rows(T); }
 
 // d_bias[n] = RNE_16 of the sum of part[range][n] in range order, 256 columns
 // per workgroup
@@ -310,9 +304,15 @@ QL_DEV void bias_fin(const BiasFin& b, int bid) {
 hipError_t launch_act8_quantize(const uint16_t* x, int64_t numel, int8_t* codes, float* scale, hipStream_t s, bool f16);
 hipError_t launch_act8_dequantize(const int8_t* codes, const float* scale, int64_t numel, uint16_t* out, hipStream_t s,
                                   bool f16);
-// the elementwise pass, with the block scales and A^T of the products behind it
-// as extra workgroups of the same launch (any of the three may be absent)
-hipError_t launch_act_bwd(const ActBwd& a, const ScalesJob& sj, const TransposeJob& tj, hipStream_t s, bool f16);
+// Splits of the two down projections of a backward and their fp32 partials.
+struct DownPair {
+    int s_g, s_p;
+    float *gpart, *ppart;
+};
+
+// the elementwise pass, with the block scales of the dX product as extra
+// workgroups of the same launch (either may be absent)
+hipError_t launch_act_bwd(const ActBwd& a, const ScalesJob& sj, hipStream_t s, bool f16);
 hipError_t launch_bias_fin(const BiasFin& b, hipStream_t s, bool f16);
 
 }  // namespace ql

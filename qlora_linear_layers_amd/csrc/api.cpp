@@ -14,9 +14,8 @@
 #include "plan.hpp"
 
 namespace ql {
-hipError_t launch_transpose_a(const uint16_t* lora_a, const LoraPlan& pl, uint8_t* ws, hipStream_t s);
-hipError_t launch_lora_down_x(const uint16_t* x, float scaling, const LoraPlan& pl, uint8_t* ws, bool transposed,
-                              hipStream_t s, bool f16);
+hipError_t launch_lora_down_x(const uint16_t* x, const uint16_t* lora_a, float scaling, const LoraPlan& pl,
+                              uint8_t* ws, bool transposed, hipStream_t s, bool f16);
 hipError_t launch_lora_down_dy(const uint16_t* dy, const uint16_t* lora_b, float scaling, const LoraPlan& pl,
                                uint8_t* ws, bool transposed, hipStream_t s, bool f16, const ScalesJob* scales);
 hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, const uint16_t* lora_b,
@@ -25,9 +24,9 @@ hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, c
 hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, const uint16_t* lora_a,
                      const LoraPlan& pl, const uint8_t* ws, uint16_t* dx, hipStream_t s, bool f16,
                      bool scales_ready, const FusedGrads* fused, const uint16_t* dx_add);
-hipError_t launch_lora_down_pair(const uint16_t* dz, const uint16_t* lora_b, const Saved& x, float scaling,
-                                 const LoraPlan& pl, uint8_t* ws, float* xpart, const BiasFin& bf, hipStream_t s,
-                                 bool f16);
+hipError_t launch_lora_down_pair(const uint16_t* dz, const uint16_t* lora_a, const uint16_t* lora_b, const Saved& x,
+                                 float scaling, const LoraPlan& pl, uint8_t* ws, const DownPair& dp,
+                                 const BiasFin& bf, hipStream_t s, bool f16);
 hipError_t launch_lora_grads(const Saved& x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws,
                              uint16_t* d_lora_a, uint16_t* d_lora_b, hipStream_t s, bool f16);
 FusedGrads fused_grads_for(const uint16_t* x, const uint16_t* dy, const LoraPlan& pl, uint8_t* ws, bool da,
@@ -162,10 +161,9 @@ int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
                                          epi ? ge : nullptr));
     }
     if (r > 0) {
-        if (int st = dev(ql::launch_transpose_a(lora_a, pl, ws, s))) return st;
         // s X A in both layouts: the transposed copy lets a backward with
         // QLORA_BWD_REUSE_FORWARD take the adapter gradients without recomputing it
-        if (int st = dev(ql::launch_lora_down_x(x, scaling, pl, ws, true, s, f16))) return st;
+        if (int st = dev(ql::launch_lora_down_x(x, lora_a, scaling, pl, ws, true, s, f16))) return st;
     }
     return dev(ql::launch_fwd(x, codes, sc, lora_b, pl, ws, y, s, f16, epi));
 }
@@ -185,8 +183,7 @@ int bwd_launch(const uint16_t* dy, const uint8_t* codes, ql::BlockScales sc, con
     }
     // s X A (both layouts) for dB when the forward's is not reused
     auto recompute_p = [&]() -> int {
-        if (int st = dev(ql::launch_transpose_a(lora_a, pl, ws, s))) return st;
-        return dev(ql::launch_lora_down_x(x, scaling, pl, ws, true, s, f16));
+        return dev(ql::launch_lora_down_x(x, lora_a, scaling, pl, ws, true, s, f16));
     };
     if (fused) {
         // dX, and the gradient partials of each 256-token tile, from one k_dx launch
@@ -343,18 +340,42 @@ int act_fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8
                     SIZE_MAX, &ep);
 }
 
-// Workspace of the backward from saved activations: the layer backward's own
-// regions, then dZ, the split partials of s X A (which run beside those of
-// s dZ B^T) and the column-sum partials of the bias gradient.
+// Plan and workspace of the backward from saved activations: the layer
+// backward's own regions, then dZ, the partials of both down projections (they
+// run in one launch) and the column-sum partials of the bias gradient.
+//
+// Down projections: up to 16 splits, for about four workgroups a CU over both
+// (each waits for memory most of its time: 4,096 tokens of an 11008 -> 4096
+// layer took 38 us with two a CU).  Adapter gradients: their workgroups hold
+// 128 KB of LDS, one a CU, so both gradients' blocks together take one round.
 struct ActBwdPlan {
     ql::LoraPlan pl;
-    size_t off_dz, off_xpart, off_part, bytes;
-    ActBwdPlan(int64_t T, int64_t K, int64_t N, int64_t r) : pl(T, K, N, r) {
+    size_t off_dz, off_gpart, off_ppart, off_part, bytes;
+    int s_g, s_p;
+    static int splits(int64_t T, int64_t L, int64_t r) {
+        const int64_t s = std::min<int64_t>(16, std::min<int64_t>(512 / ql::ceil_div(T, 64), L / 64));
+        return r > 0 ? (int)std::max<int64_t>(1, s) : 0;
+    }
+    ActBwdPlan(int64_t T, int64_t K, int64_t N, int64_t r)
+        : pl(T, K, N, r), s_g(splits(T, N, r)), s_p(splits(T, K, r)) {
         size_t o = ql::align256(std::max(pl.bwd_grad_bytes, pl.bwd_bytes));
+        const auto part = [&](int s) { return s > 1 ? (size_t)s * T * pl.r_pad * 4 : 0; };
         off_dz = o;    o = ql::align256(o + (size_t)T * N * 2);
-        off_xpart = o; o = ql::align256(o + (pl.s_down_x > 1 ? (size_t)pl.s_down_x * T * pl.r_pad * 4 : 0));
-        off_part = o;  o = ql::align256(o + (size_t)ql::act_bwd_ranges(T, N) * N * 4);
+        off_gpart = o; o = ql::align256(o + part(s_g));
+        off_ppart = o; o = ql::align256(o + part(s_p));
+        off_part = o;  o = ql::align256(o + (size_t)ql::act_bwd_ranges(T) * N * 4);
         bytes = o;
+        if (r > 0) {
+            const int64_t groups = (ql::ceil_div(K, 128) + ql::ceil_div(N, 128)) * (pl.r_pad / 64);
+            const int64_t target = std::max<int64_t>(1, 256 / groups);
+            const int cpw = (int)ql::ceil_div(T, 128 * target);
+            const int s = (int)ql::ceil_div(T, 128 * (int64_t)cpw);
+            // never more partials than the layer backward has room for
+            if (s <= pl.s_da && s <= pl.s_db) {
+                pl.cpw_da = pl.cpw_db = cpw;
+                pl.s_da = pl.s_db = s;
+            }
+        }
     }
 };
 
@@ -390,25 +411,24 @@ int act_bwd_impl(const uint16_t* dy, int64_t T, int64_t K, int64_t N, const uint
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const ql::LoraPlan& pl = ap.pl;
-    // 1: dZ, dmul and the column sums; the transposed block scales of dX and A^T
-    // of s X A ride along.  Without act and mul, dZ is dY itself.
+    // 1: dZ, dmul and the column sums, and the transposed block scales of dX.
+    // Without act and mul, dZ is dY itself.
     const bool own_dz = g->act != QLORA_ACT_NONE || sm.present();
     uint16_t* const dz_ws = reinterpret_cast<uint16_t*>(ws + ap.off_dz);
     float* const part = reinterpret_cast<float*>(ws + ap.off_part);
-    const int64_t ranges = ql::act_bwd_ranges(T, N);
+    const int64_t ranges = ql::act_bwd_ranges(T);
     const ql::ActBwd a{g->act, dy, sz, sm, own_dz ? dz_ws : nullptr, g->d_mul, g->d_bias ? part : nullptr, T, N,
-                       ql::act_bwd_rows(T, N),
+                       ql::act_bwd_rows(T),
                        own_dz || g->d_bias ? (int)(ql::ceil_div(N, 128) * ranges) : 0};
-    const ql::TransposeJob tj = grads ? ql::transpose_job_for(lora_a, pl, ws) : ql::TransposeJob{};
-    if (int st = dev(ql::launch_act_bwd(a, ql::scales_job_for(sc, pl, ws), tj, s, f16))) return st;
+    if (int st = dev(ql::launch_act_bwd(a, ql::scales_job_for(sc, pl, ws), s, f16))) return st;
     const uint16_t* dz = own_dz ? dz_ws : dy;
     // 2: s dZ B^T and s X A, and the bias gradient
     const ql::BiasFin bf{part, ranges, N, g->d_bias};
     if (r > 0) {
         const ql::Saved x = grads ? sx : ql::Saved{};
-        if (int st = dev(ql::launch_lora_down_pair(dz, lora_b, x, scaling, pl, ws,
-                                                   reinterpret_cast<float*>(ws + ap.off_xpart), bf, s, f16)))
-            return st;
+        const ql::DownPair dp{ap.s_g, ap.s_p, reinterpret_cast<float*>(ws + ap.off_gpart),
+                              reinterpret_cast<float*>(ws + ap.off_ppart)};
+        if (int st = dev(ql::launch_lora_down_pair(dz, lora_a, lora_b, x, scaling, pl, ws, dp, bf, s, f16))) return st;
     } else if (g->d_bias) {
         if (int st = dev(ql::launch_bias_fin(bf, s, f16))) return st;
     }

@@ -313,49 +313,6 @@ QL_DEV void scales_job(const ScalesJob& j, int b, lds8_t* lds) {
     }
 }
 
-// A transposed once per call, so that s X A reads the r-wide operand as rows:
-// dst[j][k] (row stride ldd) = src[k][j] for j < r, 0 for r <= j < r_pad (src
-// [K][r] bf16, r a multiple of 8).  Workgroup b takes a 64 k x 64 j tile (k tile
-// b % ceil(K / 64)): 16-byte loads of 8 j, an LDS tile, 16-byte stores of 8 k.
-// It runs alone or as extra workgroups of another launch; `lds` holds
-// kTransposeLds bytes and every thread of the 256-thread workgroup calls this.
-struct TransposeJob {
-    const uint16_t* src;
-    int64_t K, r, r_pad, ldd;
-    uint16_t* dst;
-    int blocks;               // ceil(K / 64) * r_pad / 64, 0 = no job
-};
-constexpr int kTransposeRow = 64 + 8, kTransposeLds = 64 * kTransposeRow * 2;
-QL_DEV void transpose_job(const TransposeJob& q, int b, lds8_t* lds) {
-    typedef __attribute__((address_space(3))) uint16_t lds_u16_t;
-    lds_u16_t* tile = reinterpret_cast<lds_u16_t*>(lds);              // [64 k][64 j + 8]
-    const int nk = (int)((q.K + 63) / 64);
-    const int64_t k0 = (int64_t)(b % nk) * 64, j0 = (int64_t)(b / nk) * 64;
-    const int row = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8;     // 32 rows x 8 chunks per pass
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int kk = row + 32 * h;
-        const int64_t k = k0 + kk, j = j0 + c8;
-        u32x4_t v = {0, 0, 0, 0};
-        if (k < q.K && j < q.r) v = *reinterpret_cast<const u32x4_t*>(q.src + k * q.r + j);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tile[kk * kTransposeRow + c8 + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int jj = row + 32 * h;
-        const int64_t j = j0 + jj, k = k0 + c8;
-        if (j >= q.r_pad || k >= q.K) continue;
-        u32x4_t v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = (uint32_t)tile[(c8 + 2 * e) * kTransposeRow + jj] |
-                   ((uint32_t)tile[(c8 + 2 * e + 1) * kTransposeRow + jj] << 16);
-        *reinterpret_cast<u32x4_t*>(q.dst + j * q.ldd + k) = v;
-    }
-}
-
 // One tensor of a grouped quantize or dequantize launch: `w` is read by the
 // quantizer, `out` written by the dequantizer; `absmax` set selects single
 // quantization (fp8/sup unused).
@@ -408,7 +365,6 @@ constexpr int64_t kChunkMaxT = 96;
 struct LoraPlan;
 struct Epilogue;              // output epilogue of the forward (act.hpp); one per problem of a group, or none
 ScalesJob scales_job_for(BlockScales sc, const LoraPlan& pl, uint8_t* ws);
-TransposeJob transpose_job_for(const uint16_t* lora_a, const LoraPlan& pl, uint8_t* ws);
 size_t gemv_workspace(int64_t T, int64_t K, int64_t N, int64_t r_pad);
 hipError_t launch_merge(const uint8_t* codes, BlockScales sc, const uint16_t* lora_a, const uint16_t* lora_b,
                         int64_t K, int64_t N, int64_t r, float scaling, uint16_t* w_out, hipStream_t s, bool f16);

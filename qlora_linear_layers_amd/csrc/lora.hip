@@ -16,8 +16,7 @@
 // staged through LDS in whole cache lines; the ranges of one row tile are
 // added in a fixed order by k_down_fin.  P and G leave as bf16 hi +
 // lo pairs (hi = RNE(v), lo = RNE(v - hi)), row-major for the GEMM kernels and
-// transposed for k_grad.  A is transposed once per call by k_transpose so that
-// both down projections read the r-wide operand as rows.
+// transposed for k_grad.
 //
 // k_grad: the adapter-gradient block product of grad.hpp, one 128-column x
 // 64-rank block per workgroup; token ranges of different workgroups produce
@@ -53,21 +52,13 @@ QL_DEV void split_hi_lo(float v, uint16_t& hi, uint16_t& lo) {
 
 }  // namespace
 
-// ------------------------------------------------------------------ transpose
-
-// One workgroup per 64 k x 64 j tile (see TransposeJob).
-__global__ __launch_bounds__(kThreads) void k_transpose(TransposeJob j) {
-    __shared__ __align__(16) uint8_t lds[kTransposeLds];
-    transpose_job(j, (int)blockIdx.x, (lds8_t*)lds);
-}
-
 // ------------------------------------------------------------------ down projections
 
 struct DownArgs {
     const uint16_t* s;    // [T][L] bf16 (X or dY)
     const int8_t* sc;     // or its 8-bit checkpoint: codes [T][L] and
     const float* sd;      // scales [T][L / 64]
-    const uint16_t* m;    // [m_rows][ldm] bf16 (A^T or B); rows m_rows .. r_pad-1 read as zero
+    const uint16_t* m;    // B [m_rows = r][ldm = N] bf16, or with TM A [L = K][m_rows = r]; ranks r .. r_pad-1 read as zero
     int64_t T, L, ldm, m_rows, r_pad;
     float scale;
     uint16_t* hi;         // [T][r_pad]
@@ -77,6 +68,7 @@ struct DownArgs {
     int64_t T8, ldt;
     float* part;          // [splits][T][r_pad] fp32 partial sums (splits > 1)
     int splits;
+    bool tm;              // M is A [K][r] (TM)
     ScalesJob sj;         // the dX kernel's transposed block scales, as extra workgroups (sj.blocks may be 0)
 };
 
@@ -122,7 +114,11 @@ QL_DEV void down_emit(const DownArgs& a, const float* sum, int64_t t0) {
 // Q8: S is an 8-bit checkpoint.  A round is one block of 64 codes per row, so a
 // thread loads the eight codes of its 16-byte chunk and the row's scale, and
 // rounds the eight values q d to 16 bits on their way to LDS.
-template <int RT, bool F16, bool Q8>
+//
+// TM: M is stored with the reduction as the row index (A [K][r]).  A thread
+// loads the same eight ranks of two consecutive k and writes the pairs (k, k + 1)
+// as dwords of the [rank][k] tile, so A needs no transposed copy.
+template <int RT, bool F16, bool TM, bool Q8>
 QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     constexpr int PD = RT <= 4 ? 4 : 2;
     constexpr int NX = 2;            // 16-byte chunks of the 64 x 64 S tile per thread
@@ -140,7 +136,9 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
 
     const rsrc_t rx = Q8 ? make_rsrc(a.sc, a.T * a.L) : make_rsrc(a.s, a.T * a.L * 2);
     [[maybe_unused]] const rsrc_t rd = make_rsrc(a.sd, Q8 ? a.T * a.L / 16 : 0);
-    const rsrc_t rm = make_rsrc(a.m, a.m_rows * a.ldm * 2);
+    const rsrc_t rm = make_rsrc(a.m, a.m_rows * (TM ? a.L : a.ldm) * 2);
+    const uint32_t mrow = (uint32_t)(a.m_rows * 2);                   // TM: bytes of a row of A
+    const uint32_t mround = TM ? 64u * mrow : 128u;                   // bytes of M between rounds
     uint32_t xo[NX], mo[NM];
     [[maybe_unused]] uint32_t dof[NX];
 #pragma unroll
@@ -152,9 +150,16 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     }
 #pragma unroll
     for (int u = 0; u < NM; ++u) {
-        const int q = threadIdx.x + u * kThreads;
-        const int64_t j = q >> 3;
-        mo[u] = j < a.m_rows ? (uint32_t)((j * a.ldm + (int64_t)r0 * 64 + (q & 7) * 8) * 2) : kOOB;
+        if constexpr (TM) {
+            // unit u / 2 of the thread: k pair and rank chunk; u & 1: the pair's row
+            const int e = threadIdx.x + (u >> 1) * kThreads;
+            const int pair = e / (2 * RT), jc = (e % (2 * RT)) * 8;
+            mo[u] = jc < a.m_rows ? (uint32_t)(((int64_t)r0 * 64 + 2 * pair + (u & 1)) * mrow + jc * 2) : kOOB;
+        } else {
+            const int q = threadIdx.x + u * kThreads;
+            const int64_t j = q >> 3;
+            mo[u] = j < a.m_rows ? (uint32_t)((j * a.ldm + (int64_t)r0 * 64 + (q & 7) * 8) * 2) : kOOB;
+        }
     }
     using xreg_t = std::conditional_t<Q8, u32x2_t, u32x4_t>;
     xreg_t xr[PD][NX];
@@ -162,7 +167,7 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     u32x4_t mr[PD][NM];
     auto load = [&](int i, int slot) {           // round i of this split (zeros past nr)
         const bool ok = i < nr;
-        const uint32_t so = ok ? (uint32_t)i * 128u : 0u;
+        const uint32_t so = ok ? (uint32_t)i * 128u : 0u, sm = ok ? (uint32_t)i * mround : 0u;
 #pragma unroll
         for (int u = 0; u < NX; ++u) {
             if constexpr (Q8) {
@@ -173,7 +178,7 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
             }
         }
 #pragma unroll
-        for (int u = 0; u < NM; ++u) mr[slot][u] = bload16(rm, ok ? mo[u] : kOOB, so);
+        for (int u = 0; u < NM; ++u) mr[slot][u] = bload16(rm, ok ? mo[u] : kOOB, sm);
     };
     auto store = [&](int slot, lds8_t* buf) {
 #pragma unroll
@@ -184,10 +189,24 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
             else v = xr[slot][u];
             *reinterpret_cast<lds_u32x4_t*>(buf + lds_off(q >> 3, q & 7)) = v;
         }
+        if constexpr (TM) {
 #pragma unroll
-        for (int u = 0; u < NM; ++u) {
-            const int q = threadIdx.x + u * kThreads;
-            *reinterpret_cast<lds_u32x4_t*>(buf + kXT + lds_off(q >> 3, q & 7)) = mr[slot][u];
+            for (int u = 0; u < NM; u += 2) {
+                const int e = threadIdx.x + (u >> 1) * kThreads;
+                const int pair = e / (2 * RT), jc = (e % (2 * RT)) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t sel = (i & 1) ? 0x07060302u : 0x05040100u;
+                    *reinterpret_cast<lds_u32_t*>(buf + kXT + lds_off(jc + i, pair >> 2) + (pair & 3) * 4) =
+                        __builtin_amdgcn_perm(mr[slot][u + 1][i >> 1], mr[slot][u][i >> 1], sel);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < NM; ++u) {
+                const int q = threadIdx.x + u * kThreads;
+                *reinterpret_cast<lds_u32x4_t*>(buf + kXT + lds_off(q >> 3, q & 7)) = mr[slot][u];
+            }
         }
     };
 
@@ -244,7 +263,7 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     }
 }
 
-template <int RT, bool F16>
+template <int RT, bool F16, bool TM>
 __global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const int n = (int)ceil_div(a.T, 64) * a.splits, bid = (int)blockIdx.x;
@@ -252,7 +271,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_down(DownArgs a) {
         scales_job(a.sj, bid - n, (lds8_t*)smem_raw);     // after the longer projection workgroups
         return;
     }
-    down_block<RT, F16, false>(a, bid, smem_raw);
+    down_block<RT, F16, TM, false>(a, bid, smem_raw);
 }
 
 // Both down projections of a backward in one launch, then the sums of the bias
@@ -262,8 +281,8 @@ template <int RT, bool F16, bool Q8>
 __global__ __launch_bounds__(kThreads, 2) void k_down2(DownArgs a0, DownArgs a1, int n0, int n1, BiasFin bf) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const int bid = (int)blockIdx.x;
-    if (bid < n0) down_block<RT, F16, false>(a0, bid, smem_raw);
-    else if (bid < n0 + n1) down_block<RT, F16, Q8>(a1, bid - n0, smem_raw);
+    if (bid < n0) down_block<RT, F16, false, false>(a0, bid, smem_raw);
+    else if (bid < n0 + n1) down_block<RT, F16, true, Q8>(a1, bid - n0, smem_raw);
     else bias_fin<F16>(bf, bid - n0 - n1);
 }
 
@@ -276,15 +295,19 @@ QL_DEV void down_fin_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     for (int e = threadIdx.x; e < 4 * R; e += kThreads) {
         const int tl = e / (R / 4), j = 4 * (e % (R / 4));
         const int64_t t = t0 + tl;
-        f32x4_t v[8];
+        f32x4_t s4 = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s0 = 0; s0 < a.splits; s0 += 8) {                // eight loads issued together
+            f32x4_t v[8];
 #pragma unroll
-        for (int sp = 0; sp < 8; ++sp)                            // splits <= 8: loads issued together
-            v[sp] = (sp < a.splits && t < a.T)
-                        ? *reinterpret_cast<const f32x4_t*>(a.part + ((int64_t)sp * a.T + t) * a.r_pad + j)
-                        : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        f32x4_t s4 = v[0];
+            for (int q = 0; q < 8; ++q) {
+                const int sp = s0 + q;
+                v[q] = (sp < a.splits && t < a.T)
+                           ? *reinterpret_cast<const f32x4_t*>(a.part + ((int64_t)sp * a.T + t) * a.r_pad + j)
+                           : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            }
 #pragma unroll
-        for (int sp = 1; sp < 8; ++sp) s4 += v[sp];
+            for (int q = 0; q < 8; ++q) s4 += v[q];
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) sum[tl * (R + 4) + j + c] = s4[c];
     }
@@ -394,14 +417,16 @@ hipError_t down_rt(const DownArgs& a, hipStream_t s) {
     constexpr int R = RT * 16;
     const size_t bufs = (size_t)2 * (64 + R) * 128, sums = (size_t)64 * (R + 4) * 4;
     const size_t lds = bufs > sums ? bufs : sums;
-    hipError_t e = set_smem(k_down<RT, F16>, lds);
-    if (e != hipSuccess) return e;
     const unsigned tiles = (unsigned)ceil_div(a.T, 64);
-    hipLaunchKernelGGL((k_down<RT, F16>), dim3(tiles * (unsigned)a.splits + (unsigned)a.sj.blocks), dim3(kThreads),
-                       lds, s, a);
-    if (a.splits > 1) {
-        e = hipGetLastError();
+    auto go = [&](auto kern) {
+        hipError_t e = set_smem(kern, lds);
         if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kern, dim3(tiles * (unsigned)a.splits + (unsigned)a.sj.blocks), dim3(kThreads), lds, s, a);
+        return hipGetLastError();
+    };
+    hipError_t e = a.tm ? go(k_down<RT, F16, true>) : go(k_down<RT, F16, false>);
+    if (e != hipSuccess) return e;
+    if (a.splits > 1) {
         const size_t fl = (size_t)16 * (R + 4) * 4;
         const int n = (int)ceil_div(a.T, 16);
         hipLaunchKernelGGL((k_down_fin<RT, F16>), dim3((unsigned)n), dim3(kThreads), fl, s, a, a, n);
@@ -487,27 +512,16 @@ hipError_t grad_finalize(GradFin fa, bool has_a, const GradFin& fb, bool has_b, 
 
 }  // namespace
 
-TransposeJob transpose_job_for(const uint16_t* lora_a, const LoraPlan& pl, uint8_t* ws) {
-    return TransposeJob{lora_a, pl.K, pl.r, pl.r_pad, pl.ld_at, reinterpret_cast<uint16_t*>(ws + pl.off_at),
-                        (int)(ceil_div(pl.K, 64) * (pl.r_pad / 64))};
-}
-
-hipError_t launch_transpose_a(const uint16_t* lora_a, const LoraPlan& pl, uint8_t* ws, hipStream_t s) {
-    const TransposeJob j = transpose_job_for(lora_a, pl, ws);
-    hipLaunchKernelGGL(k_transpose, dim3((unsigned)j.blocks), dim3(kThreads), 0, s, j);
-    return hipGetLastError();
-}
-
 namespace {
 
-// s X A -> P (hi/lo [T][r_pad]; also transposed when `transposed`).  Needs A^T in ws.
-DownArgs down_x_args(const Saved& x, float scaling, const LoraPlan& pl, uint8_t* ws, bool transposed) {
-    return DownArgs{x.v, x.codes, x.scale, reinterpret_cast<const uint16_t*>(ws + pl.off_at), pl.T, pl.K, pl.ld_at,
-                    pl.r_pad, pl.r_pad, scaling,
+// s X A -> P (hi/lo [T][r_pad]; also transposed when `transposed`)
+DownArgs down_x_args(const Saved& x, const uint16_t* lora_a, float scaling, const LoraPlan& pl, uint8_t* ws,
+                     bool transposed) {
+    return DownArgs{x.v, x.codes, x.scale, lora_a, pl.T, pl.K, pl.r, pl.r, pl.r_pad, scaling,
                     reinterpret_cast<uint16_t*>(ws + pl.off_ps_hi), reinterpret_cast<uint16_t*>(ws + pl.off_ps_lo),
                     transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_pst_hi) : nullptr,
                     transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_pst_lo) : nullptr, pl.T8, pl.ld_t,
-                    reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_x, ScalesJob{}};
+                    reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_x, true, ScalesJob{}};
 }
 
 // s dY B^T -> G (hi/lo [T][r_pad], also transposed when `transposed`)
@@ -517,14 +531,14 @@ DownArgs down_dy_args(const uint16_t* dy, const uint16_t* lora_b, float scaling,
                     reinterpret_cast<uint16_t*>(ws + pl.off_gs_hi), reinterpret_cast<uint16_t*>(ws + pl.off_gs_lo),
                     transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_gst_hi) : nullptr,
                     transposed ? reinterpret_cast<uint16_t*>(ws + pl.off_gst_lo) : nullptr, pl.T8, pl.ld_t,
-                    reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_dy, ScalesJob{}};
+                    reinterpret_cast<float*>(ws + pl.off_dpart), pl.s_down_dy, false, ScalesJob{}};
 }
 
 }  // namespace
 
-hipError_t launch_lora_down_x(const uint16_t* x, float scaling, const LoraPlan& pl, uint8_t* ws, bool transposed,
-                              hipStream_t s, bool f16) {
-    return down(down_x_args(Saved{x, nullptr, nullptr}, scaling, pl, ws, transposed), s, f16);
+hipError_t launch_lora_down_x(const uint16_t* x, const uint16_t* lora_a, float scaling, const LoraPlan& pl,
+                              uint8_t* ws, bool transposed, hipStream_t s, bool f16) {
+    return down(down_x_args(Saved{x, nullptr, nullptr}, lora_a, scaling, pl, ws, transposed), s, f16);
 }
 
 // `scales` (if not NULL) runs as extra workgroups of the same launch.
@@ -535,16 +549,18 @@ hipError_t launch_lora_down_dy(const uint16_t* dy, const uint16_t* lora_b, float
     return down(a, s, f16);
 }
 
-// G and, with `x` present, P (needs A^T in ws), both transposed too then; and
-// the bias gradient.  The two projections' split partials need room of their
-// own: P's follow G's at `xpart`.
-hipError_t launch_lora_down_pair(const uint16_t* dz, const uint16_t* lora_b, const Saved& x, float scaling,
-                                 const LoraPlan& pl, uint8_t* ws, float* xpart, const BiasFin& bf, hipStream_t s,
-                                 bool f16) {
+// G and, with `x` present, P, both transposed too then; and the bias gradient.
+// `splits` ranges of each reduction, whose partials are at gpart and ppart.
+hipError_t launch_lora_down_pair(const uint16_t* dz, const uint16_t* lora_a, const uint16_t* lora_b, const Saved& x,
+                                 float scaling, const LoraPlan& pl, uint8_t* ws, const DownPair& dp,
+                                 const BiasFin& bf, hipStream_t s, bool f16) {
     const bool second = x.present();
-    const DownArgs a0 = down_dy_args(dz, lora_b, scaling, pl, ws, second);
-    DownArgs a1 = down_x_args(x, scaling, pl, ws, true);
-    a1.part = xpart;
+    DownArgs a0 = down_dy_args(dz, lora_b, scaling, pl, ws, second);
+    DownArgs a1 = down_x_args(x, lora_a, scaling, pl, ws, true);
+    a0.part = dp.gpart;
+    a0.splits = dp.s_g;
+    a1.part = dp.ppart;
+    a1.splits = dp.s_p;
     return f16 ? down2_t<true>(a0, a1, second, bf, s) : down2_t<false>(a0, a1, second, bf, s);
 }
 

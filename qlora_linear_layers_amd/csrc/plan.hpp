@@ -73,12 +73,11 @@ constexpr size_t kSplitPartialMax = size_t(64) << 20;
 struct LoraPlan {
     int64_t T, K, N, r, r_pad, T8;
     int s_down_x, s_down_dy;   // reduction splits of s X A and s dY B^T
-    int64_t ld_at, ld_t;   // row strides of A^T and of the transposed intermediates (padded by 64)
+    int64_t ld_t;          // row stride of the transposed intermediates (padded by 64)
     int s_da, cpw_da;    // dA = X^T G: token splits, chunks per wave
     int s_db, cpw_db;    // dB = P^T dY
 
     // byte offsets inside the workspace
-    size_t off_at;                      // A^T, bf16 [r_pad][ld_at] (rows >= r zero)
     size_t off_ps_hi, off_ps_lo;        // P = s X A as bf16 hi/lo, [T][r_pad] each
     size_t off_gs_hi, off_gs_lo;        // G = s dY B^T as bf16 hi/lo, [T][r_pad] each
     size_t off_scl;                     // block scales c1', fp32 transposed [K/64][N] (dX)
@@ -110,7 +109,6 @@ struct LoraPlan {
         T8 = ceil_div(T, 8) * 8;
         // a 128-byte shift per row keeps the same column of consecutive rows off
         // one memory channel
-        ld_at = K + 64;
         ld_t = T8 + 64;
         cpw_da = cpw_db = 1;
         s_down_x = down_splits(T, K);
@@ -127,7 +125,7 @@ struct LoraPlan {
         const size_t dxp = s_dx > 1 ? align256((size_t)s_dx * K * split_row(T) * 4) : 0;
         if (r == 0) {
             const size_t fsp = splits_within(0);
-            off_at = off_ps_hi = off_ps_lo = off_gs_hi = off_gs_lo = 0;
+            off_ps_hi = off_ps_lo = off_gs_hi = off_gs_lo = 0;
             off_pst_hi = off_pst_lo = off_gst_hi = off_gst_lo = off_pda = off_pdb = 0;
             off_dpart = 0;
             off_scl = 0;
@@ -141,8 +139,7 @@ struct LoraPlan {
         }
         const size_t tr2 = (size_t)T * r_pad * 2, rt2 = (size_t)r_pad * ld_t * 2;
         size_t o = 0;
-        // forward: A^T, s X A (both layouts, kept for the backward), split partials
-        off_at = o;     o = align256(o + (size_t)r_pad * ld_at * 2);
+        // forward: s X A (both layouts, kept for the backward), split partials
         off_ps_hi = o;  o = align256(o + tr2);
         off_ps_lo = o;  o = align256(o + tr2);
         off_pst_hi = o; o = align256(o + rt2);
