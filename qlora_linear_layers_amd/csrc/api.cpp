@@ -158,7 +158,7 @@ int fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8_t* 
             if (epi) ge[c] = epilogue_rows(*epi, t0, N);
         }
         return dev(ql::launch_gemv_group(g, (int)windows, ql::kGemvMaxT, r, ws, s, f16, ql::DecodeProduct::Auto,
-                                         epi ? ge : nullptr));
+                                         epi ? ge : nullptr, true));
     }
     if (r > 0) {
         // s X A in both layouts: the transposed copy lets a backward with

@@ -386,6 +386,8 @@ struct GemvProblem {
     uint16_t* y;
     int64_t skip = 0;     // leading token rows computed but not written (another problem writes them)
 };
+// windows: the problems are the 16-token windows of one weight (same codes,
+// scales, adapter, K and N), whose base products share one pass over it.
 size_t gemv_group_workspace(const GemvProblem* probs, int count, int64_t T, int64_t r_pad);
 // The decode product: on the matrix cores (16 token rows, padded) or as VALU
 // dot products (T <= kGemvValuMaxT; bf16 with double quantization); Auto is the
@@ -393,6 +395,7 @@ size_t gemv_group_workspace(const GemvProblem* probs, int count, int64_t T, int6
 enum class DecodeProduct { Auto, Mfma, Valu };
 constexpr int64_t kGemvValuMaxT = 8;
 hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int64_t r, uint8_t* ws, hipStream_t s,
-                             bool f16, DecodeProduct prod = DecodeProduct::Auto, const Epilogue* epis = nullptr);
+                             bool f16, DecodeProduct prod = DecodeProduct::Auto, const Epilogue* epis = nullptr,
+                             bool windows = false);
 
 }  // namespace ql

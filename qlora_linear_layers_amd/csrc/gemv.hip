@@ -363,6 +363,112 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
     }
 }
 
+// Launch 1 of a chunked call (16 < T <= kChunkMaxT): G windows of 16 tokens
+// of one weight, the problems of `grp`.  A base block does the work of k_gemv's
+// block for every window at once: the codes are loaded and dequantized once and
+// each weight fragment meets G token fragments (4 G MFMAs per 64 rows x 32 k and
+// lane, against four), so the weight stream and the dequantization do not grow
+// with T.  4096 x 4096 at 61 tokens (no adapter): 20.7 us as four windows of
+// k_gemv, whose VALU work is four dequantizations of the weight.  Sums and
+// their order are those of k_gemv, so are the partials.  The k waves of a row
+// group are added one window at a time, alternating two 32 KB LDS buffers (one
+// over the table), one barrier per window.
+template <int G, bool SQ, bool F16>
+__global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Codebook cb) {
+    extern __shared__ __align__(16) uint8_t dyn[];
+    const int bid = (int)blockIdx.x;
+    const int lora_total = grp.lora_end[grp.count - 1];
+    if (bid < lora_total) {
+        const int i = group_find(grp.lora_end, grp.count, bid);
+        const GemvArgs p = grp.p[i];
+        lora_down_block<kGemvMaxT, F16>(p, dyn, bid - (i ? grp.lora_end[i - 1] : 0));
+        return;
+    }
+    const GemvArgs p = grp.p[0];                                       // the weight of every window
+    const int bx = bid - lora_total;
+    lds8_t* tbl = (lds8_t*)dyn;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = wv % kKW, rg = wv / kKW;                          // k step, row group
+    const int nl = lane & 15, g = lane >> 4;
+    const int nb = (int)ceil_div(p.N, kDecRows);
+    const int rb = bx % nb, ks = bx / nb;
+    const int64_t n0 = (int64_t)rb * kDecRows + 64 * rg;
+    const int64_t kk = (int64_t)ks * kDecK + 128 * wave + 32 * g;      // this lane's 32 k
+    const bool kok = kk < p.K;
+    const rsrc_t rc = make_rsrc(p.codes, p.N * p.K / 2);
+    const rsrc_t rf = SQ ? make_rsrc(p.absmax, p.N * p.K / 64 * 4) : make_rsrc(p.fp8, p.N * p.K / 64);
+    const rsrc_t rs = SQ ? rf : make_rsrc(p.sup, ceil_div(p.N * p.K / 64, 256) * 4);
+
+    u32x4_t cw[4], xv[G][4];
+    uint32_t f8[4], s2[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int64_t n = n0 + 16 * c + nl;
+        const bool ok = kok && n < p.N;
+        const int64_t blk = n * (p.K / 64) + kk / 64;
+        cw[c] = bload16(rc, ok ? (uint32_t)(n * (p.K / 2) + kk / 2) : kOOB, 0);
+        if constexpr (SQ) {
+            f8[c] = 0;
+            s2[c] = bload4(rf, ok ? (uint32_t)blk * 4u : kOOB, 0);
+        } else {
+            f8[c] = bload1(rf, ok ? (uint32_t)blk : kOOB, 0);
+            s2[c] = bload4(rs, ok ? (uint32_t)(blk >> 8) * 4u : kOOB, 0);
+        }
+    }
+    // token nl of every window (all windows are full)
+    const uint32_t xo = kok ? (uint32_t)((nl * p.K + kk) * 2) : kOOB;
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+        const rsrc_t rx = make_rsrc(grp.p[q].x, kGemvMaxT * p.K * 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xv[q][j] = bload16(rx, xo, (uint32_t)(16 * j));
+    }
+    if (threadIdx.x < 256) build_pair_table16(tbl, cb);
+    __syncthreads();
+
+    const uint32_t lane8 = lds_addr(tbl) + (uint32_t)(lane & 15) * 8u;
+    f32x4_t acc[G][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float c1p = SQ ? __uint_as_float(s2[c]) : block_scale(f8[c], __uint_as_float(s2[c]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u32x4_t w;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f32x2_t q = *lds_at<f32x2_t>((__builtin_amdgcn_ubfe(cw[c][j], 8 * b, 8) << 7) | lane8);
+                w[b] = pack16x2<F16>(__fmul_rn(q[0], c1p), __fmul_rn(q[1], c1p));
+            }
+#pragma unroll
+            for (int q = 0; q < G; ++q) {
+                const f32x4_t a = j == 0 ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : acc[q][c];
+                acc[q][c] = mfma16x16x32<F16>(__builtin_bit_cast(bf16x8_t, xv[q][j]), __builtin_bit_cast(bf16x8_t, w), a);
+            }
+        }
+    }
+
+    __syncthreads();                                                   // the table is no longer read
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+        f32x4_t* red = reinterpret_cast<f32x4_t*>(dyn + (q & 1) * kNarrowTableBytes) + rg * (kKW * 4 * 64);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) red[(wave * 4 + c) * 64 + lane] = acc[q][c];
+        __syncthreads();                       // also: buffer q & 1 was read before the barrier of window q - 1
+        if (wave < 4) {
+            const int c = wave, l = lane;
+            f32x4_t v = red[c * 64 + l];
+#pragma unroll
+            for (int w = 1; w < kKW; ++w) v += red[(w * 4 + c) * 64 + l];
+            const int64_t n = n0 + 16 * c + (l & 15);
+            float* part = grp.p[q].part + (int64_t)ks * kGemvMaxT * p.N;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n < p.N) part[(int64_t)(4 * (l >> 4) + e) * p.N + n] = v[e];
+        }
+    }
+}
+
 // Launch 2.  Y[t][n] = sum_ks part[ks][t][n] + sum_j u[t][j] B[j][n] with
 // u = s X A rebuilt from its slice partials, rounded to the 16-bit type.  A
 // workgroup owns 128 columns up to T = 8 (two adjacent ones per lane: N is a
@@ -633,8 +739,9 @@ size_t gemv_group_workspace(const GemvProblem* probs, int count, int64_t T, int6
 }
 
 hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int64_t r, uint8_t* ws, hipStream_t s,
-                             bool f16, DecodeProduct prod, const Epilogue* epis) {
+                             bool f16, DecodeProduct prod, const Epilogue* epis, bool windows) {
     if (count < 1 || count > kMaxGroup) return hipErrorInvalidValue;
+    if (windows && (T != kGemvMaxT || prod != DecodeProduct::Auto)) return hipErrorInvalidValue;
     if (prod == DecodeProduct::Valu && T > kGemvValuMaxT) return hipErrorInvalidValue;
     const bool dot = prod == DecodeProduct::Valu;
     const int64_t r_pad = r > 0 ? ceil_div(r, 64) * 64 : 0;
@@ -661,13 +768,14 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     const bool sq = probs[0].sc.single();
     if (dot && (sq || f16)) return hipErrorInvalidValue;             // the VALU form serves the bf16 DQ path
     const Codebook& cb = host_codebook();
-    const dim3 grid((unsigned)(nl + nbase));
+    const dim3 grid((unsigned)(nl + (windows ? g.p[0].gemv_blocks : nbase)));
     hipError_t ae = hipSuccess;
     size_t lds = dot ? kDecLds : (size_t)kNarrowTableBytes;
     auto go = [&](auto kern) {
-        // 64 KB (and more) of dynamic LDS: above the default limit
-        ae = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)lds);
+        // more than 64 KB of dynamic LDS: above the default limit
+        if (lds > 65536)
+            ae = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)lds);
         if (ae == hipSuccess) hipLaunchKernelGGL(kern, grid, dim3(kDecThreads), lds, s, g, cb);
     };
     auto pick = [&](auto tt) {
@@ -682,7 +790,23 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
         if (sq) f16 ? go(k_gemv<TT, true, true, false>) : go(k_gemv<TT, true, false, false>);
         else f16 ? go(k_gemv<TT, false, true, false>) : go(k_gemv<TT, false, false, false>);
     };
-    if (T <= 1) pick(std::integral_constant<int, 1>{});
+    auto pick_win = [&](auto gg) {
+        constexpr int G = decltype(gg)::value;
+        lds = 2 * (size_t)kNarrowTableBytes;
+        if (sq) f16 ? go(k_gemv_win<G, true, true>) : go(k_gemv_win<G, true, false>);
+        else f16 ? go(k_gemv_win<G, false, true>) : go(k_gemv_win<G, false, false>);
+    };
+    if (windows) {
+        static_assert(kChunkMaxT / kGemvMaxT == 6, "one instance per window count");
+        switch (count) {
+            case 2: pick_win(std::integral_constant<int, 2>{}); break;
+            case 3: pick_win(std::integral_constant<int, 3>{}); break;
+            case 4: pick_win(std::integral_constant<int, 4>{}); break;
+            case 5: pick_win(std::integral_constant<int, 5>{}); break;
+            case 6: pick_win(std::integral_constant<int, 6>{}); break;
+            default: return hipErrorInvalidValue;
+        }
+    } else if (T <= 1) pick(std::integral_constant<int, 1>{});
     else if (T <= 2) pick(std::integral_constant<int, 2>{});
     else if (T <= 4) pick(std::integral_constant<int, 4>{});
     else if (T <= 8) pick(std::integral_constant<int, 8>{});

@@ -213,15 +213,40 @@ QL_DEV void down_block(const DownArgs& a, int bid, uint8_t* smem_raw) {
     f32x4_t acc[RT];
 #pragma unroll
     for (int jt = 0; jt < RT; ++jt) acc[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    // Up to 128 ranks the fragments of a round (64 ranks) or step are read before
+    // its first MFMA: the compiler would otherwise reuse one register set and
+    // wait out an LDS latency in front of every MFMA (5-10% of the launch).
+    // Above that they do not fit the registers.
     auto compute = [&](const lds8_t* buf) {
+        auto xfrag = [&](int st) {
+            return *reinterpret_cast<const lds_bf16x8_t*>(buf + lds_off(16 * w + (l & 15), 4 * st + (l >> 4)));
+        };
+        auto mfrag = [&](int st, int jt) {
+            return *reinterpret_cast<const lds_bf16x8_t*>(buf + kXT + lds_off(16 * jt + (l & 15), 4 * st + (l >> 4)));
+        };
+        if constexpr (RT <= 8) {
+            constexpr int G = RT <= 4 ? 2 : 1;   // steps read together
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            const int ch = 4 * st + (l >> 4);
-            const bf16x8_t xv = *reinterpret_cast<const lds_bf16x8_t*>(buf + lds_off(16 * w + (l & 15), ch));
+            for (int s0 = 0; s0 < 2; s0 += G) {
+                bf16x8_t xv[G], mv[G][RT];
 #pragma unroll
-            for (int jt = 0; jt < RT; ++jt) {
-                const bf16x8_t mv = *reinterpret_cast<const lds_bf16x8_t*>(buf + kXT + lds_off(16 * jt + (l & 15), ch));
-                acc[jt] = mfma16<F16>(xv, mv, acc[jt]);
+                for (int g = 0; g < G; ++g) {
+                    xv[g] = xfrag(s0 + g);
+#pragma unroll
+                    for (int jt = 0; jt < RT; ++jt) mv[g][jt] = mfrag(s0 + g, jt);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int jt = 0; jt < RT; ++jt) acc[jt] = mfma16<F16>(xv[g], mv[g][jt], acc[jt]);
+            }
+        } else {
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const bf16x8_t xv = xfrag(st);
+#pragma unroll
+                for (int jt = 0; jt < RT; ++jt) acc[jt] = mfma16<F16>(xv, mfrag(st, jt), acc[jt]);
             }
         }
     };
