@@ -150,7 +150,7 @@ def _stream():
 
 
 def _dev(t, dtype, name):
-    if t is None:
+    if t is None or (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -620,9 +620,9 @@ class Act8:
 
 def _check_act8(a8, name):
     """The checkpoint's tensors must hold exactly what its shape needs."""
-    n = a8.numel
-    _count(a8.codes, n, f"{name} codes")
-    _count(a8.scale, -(-n // 64), f"{name} scale")
+    n = math.prod(a8.shape)
+    _count(a8.codes, n, name + " codes")
+    _count(a8.scale, -(-n // 64), name + " scale")
 
 
 def act8_empty(shape, device="cuda"):
@@ -634,31 +634,32 @@ def act8_empty(shape, device="cuda"):
 
 def act8_quantize(x, out=None):
     """bf16 or fp16 activation of any shape -> Act8 (written into `out` if given)."""
-    ct = _ct(x, "x")
+    fn = "act8_quantize" + _ct(x, "x")
     if out is not None:
         _check_act8(out, "out")
         _shape(x, out.shape, "x")
-    _dev(x, x.dtype, "x")
-    if out is None:
+        _dev(x, x.dtype, "x")
+        _dev(out.codes, torch.int8, "out codes")
+        _dev(out.scale, torch.float32, "out scale")
+    else:
+        _dev(x, x.dtype, "x")
         out = act8_empty(x.shape, x.device)
-    _dev(out.codes, torch.int8, "out codes")
-    _dev(out.scale, torch.float32, "out scale")
-    fn = "act8_quantize" + ct
-    _check(fn, getattr(lib(), fn)(_ptr(x), x.numel(), _ptr(out.codes), _ptr(out.scale), _stream()))
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), x.numel(), out.codes.data_ptr(), out.scale.data_ptr(), _stream()))
     return out
 
 
 def act8_dequantize(a8, dtype=torch.bfloat16, out=None):
     """Act8 -> the 16-bit values it stands for, in `dtype` (or in the dtype of `out`)."""
     _check_act8(a8, "checkpoint")
+    codes, scale = a8.codes, a8.scale
     _shape(out, a8.shape, "out")
-    _dev(a8.codes, torch.int8, "codes")
-    _dev(a8.scale, torch.float32, "scale")
+    _dev(codes, torch.int8, "codes")
+    _dev(scale, torch.float32, "scale")
     if out is None:
-        out = torch.empty(a8.shape, dtype=dtype, device=a8.codes.device)
+        out = torch.empty(a8.shape, dtype=dtype, device=codes.device)
     fn = "act8_dequantize" + _ct(out, "out")
     _dev(out, out.dtype, "out")
-    _check(fn, getattr(lib(), fn)(_ptr(a8.codes), _ptr(a8.scale), a8.numel, _ptr(out), _stream()))
+    _check(fn, getattr(lib(), fn)(codes.data_ptr(), scale.data_ptr(), codes.numel(), out.data_ptr(), _stream()))
     return out
 
 
@@ -677,37 +678,47 @@ def qlora_linear_act_fwd(x, qw, lora_a=None, lora_b=None, scaling=1.0, bias=None
     _check_storage(qw)
     if x.dim() != 2:
         raise ValueError(f"x must be 2-D [T, K], got shape {tuple(x.shape)}")
-    T, N = x.shape[0], qw.N
-    _shape(x, (T, qw.K), "x")
-    r = _check_adapters(lora_a, lora_b, qw.K, N)
+    T, N, K = x.shape[0], qw.N, qw.K
+    _shape(x, (T, K), "x")
+    r = _check_adapters(lora_a, lora_b, K, N)
     _shape(bias, (N,), "bias")
-    for t, name in ((mul, "mul"), (residual, "residual"), (out, "out")):
-        _shape(t, (T, N), name)
+    _shape(mul, (T, N), "mul")
+    _shape(residual, (T, N), "residual")
+    _shape(out, (T, N), "out")
     if z is not None:
         if save == "z8":
             _check_act8(z, "z")
         if tuple(z.shape) != (T, N):
             raise ValueError(f"z has shape {tuple(z.shape)}, expected {(T, N)}")
-    for t, name in ((x, "x"), (lora_a, "lora_a"), (lora_b, "lora_b"), (bias, "bias"), (mul, "mul"),
-                    (residual, "residual"), (out, "out")):
-        _dev(t, x.dtype, name)
+    dt = x.dtype
+    _dev(x, dt, "x")
+    _dev(lora_a, dt, "lora_a")
+    _dev(lora_b, dt, "lora_b")
+    _dev(bias, dt, "bias")
+    _dev(mul, dt, "mul")
+    _dev(residual, dt, "residual")
+    _dev(out, dt, "out")
     if out is None:
-        out = torch.empty((T, N), dtype=x.dtype, device=x.device)
-    if save and z is None:
-        z = act8_empty((T, N), x.device) if save == "z8" else torch.empty_like(out)
+        out = torch.empty((T, N), dtype=dt, device=x.device)
+    z16 = zc = zs = None
     if save == "z8":
+        if z is None:
+            z = act8_empty((T, N), x.device)
         _dev(z.codes, torch.int8, "z codes")
         _dev(z.scale, torch.float32, "z scale")
+        zc, zs = z.codes.data_ptr(), z.scale.data_ptr()
     elif save:
-        _dev(z, x.dtype, "z")
+        if z is None:
+            z = torch.empty_like(out)
+        _dev(z, dt, "z")
+        z16 = z.data_ptr()
     if workspace is None:
-        workspace = workspace_for(T, qw.K, N, r, x.device)
-    ep = Epilogue(code, _ptr(bias), _ptr(mul), _ptr(residual), _ptr(z) if save == "z" else None,
-                  _ptr(z.codes) if save == "z8" else None, _ptr(z.scale) if save == "z8" else None)
+        workspace = workspace_for(T, K, N, r, x.device)
+    ep = Epilogue(code, _ptr(bias), _ptr(mul), _ptr(residual), z16, zc, zs)
     fn = _entry("qlora_linear_act_fwd", ct, qw)
     _check(fn, getattr(lib(), fn)(
-        _ptr(x), T, qw.K, N, _ptr(qw.codes), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r, float(scaling),
-        ctypes.byref(ep), _ptr(out), _ptr(workspace), workspace.numel(), _stream()))
+        x.data_ptr(), T, K, N, qw.codes.data_ptr(), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r,
+        float(scaling), ctypes.byref(ep), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream()))
     return (out, z) if save else out
 
 
@@ -725,23 +736,37 @@ def qlora_act_workspace_bytes_bwd(T, K, N, r):
     return int(lib().qlora_act_workspace_bytes_bwd(T, K, N, r))
 
 
-def _saved(v, shape, dtype, name):
-    """Checks of one saved activation (tensor or Act8) against its shape."""
+_ABSENT = Saved()
+
+
+def _saved(v, shape, name):
+    """Checks of one saved activation (tensor, Act8 or None) against its shape."""
     if isinstance(v, Act8):
         _check_act8(v, name)
-        if tuple(v.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(v.shape)}, expected {tuple(shape)}")
+        if tuple(v.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(v.shape)}, expected {shape}")
     else:
         _shape(v, shape, name)
 
 
 def _saved_arg(v, dtype, name):
+    """The C argument of a checked saved activation."""
+    if v is None:
+        return _ABSENT
     if isinstance(v, Act8):
         _dev(v.codes, torch.int8, name + " codes")
         _dev(v.scale, torch.float32, name + " scale")
         return Saved(None, v.codes.data_ptr(), v.scale.data_ptr())
     _dev(v, dtype, name)
-    return Saved(_ptr(v), None, None)
+    return Saved(v.data_ptr(), None, None)
+
+
+def _grad_out(t, shape, asked, name):
+    """Checks of a caller's gradient tensor, which is given only if it is asked for."""
+    if t is not None:
+        if not asked:
+            raise ValueError(f"{name} is given but its gradient is not asked for")
+        _shape(t, shape, name)
 
 
 def qlora_linear_act_bwd(dy, qw, lora_a=None, lora_b=None, scaling=1.0, act="none", x=None, z=None, mul=None,
@@ -767,42 +792,41 @@ def qlora_linear_act_bwd(dy, qw, lora_a=None, lora_b=None, scaling=1.0, act="non
         raise ValueError("lora_grads needs x")
     if z is None and (code or mul_grad):
         raise ValueError("an activation or the gradient of mul needs z")
-    _saved(x, (T, K), dy.dtype, "x")
-    _saved(z, (T, N), dy.dtype, "z")
-    _saved(mul, (T, N), dy.dtype, "mul")
+    _saved(x, (T, K), "x")
+    _saved(z, (T, N), "z")
+    _saved(mul, (T, N), "mul")
     _shape(dx_add, (T, K), "dx_add")
-    outs = {"dx": (dx, (T, K), True), "d_lora_a": (d_lora_a, (K, r), lora_grads),
-            "d_lora_b": (d_lora_b, (r, N), lora_grads), "d_bias": (d_bias, (N,), bias_grad),
-            "d_mul": (d_mul, (T, N), mul_grad)}
-    for name, (t, shape, asked) in outs.items():
-        if t is not None and not asked:
-            raise ValueError(f"{name} is given but its gradient is not asked for")
-        _shape(t, shape, name)
-    for t, name in ((dy, "dy"), (lora_a, "lora_a"), (lora_b, "lora_b"), (dx_add, "dx_add")):
-        _dev(t, dy.dtype, name)
-    g = ActGrad(act=code, dx_add=_ptr(dx_add))
-    if x is not None:
-        g.x = _saved_arg(x, dy.dtype, "x")
-    if z is not None:
-        g.z = _saved_arg(z, dy.dtype, "z")
-    if mul is not None:
-        g.mul = _saved_arg(mul, dy.dtype, "mul")
-    res = {}
-    for name, (t, shape, asked) in outs.items():
-        if asked:
-            if t is None:
-                t = torch.empty(shape, dtype=dy.dtype, device=dy.device)
-            _dev(t, dy.dtype, name)
-            setattr(g, name, t.data_ptr())
-            res[name] = t
+    _shape(dx, (T, K), "dx")
+    _grad_out(d_lora_a, (K, r), lora_grads, "d_lora_a")
+    _grad_out(d_lora_b, (r, N), lora_grads, "d_lora_b")
+    _grad_out(d_bias, (N,), bias_grad, "d_bias")
+    _grad_out(d_mul, (T, N), mul_grad, "d_mul")
+    dt, device = dy.dtype, dy.device
+    for t, name in ((dy, "dy"), (lora_a, "lora_a"), (lora_b, "lora_b"), (dx_add, "dx_add"), (dx, "dx"),
+                    (d_lora_a, "d_lora_a"), (d_lora_b, "d_lora_b"), (d_bias, "d_bias"), (d_mul, "d_mul")):
+        _dev(t, dt, name)
+    sx, sz, sm = _saved_arg(x, dt, "x"), _saved_arg(z, dt, "z"), _saved_arg(mul, dt, "mul")
+    if dx is None:
+        dx = torch.empty((T, K), dtype=dt, device=device)
+    if lora_grads:
+        if d_lora_a is None:
+            d_lora_a = torch.empty((K, r), dtype=dt, device=device)
+        if d_lora_b is None:
+            d_lora_b = torch.empty((r, N), dtype=dt, device=device)
+    if bias_grad and d_bias is None:
+        d_bias = torch.empty((N,), dtype=dt, device=device)
+    if mul_grad and d_mul is None:
+        d_mul = torch.empty((T, N), dtype=dt, device=device)
     if workspace is None:
         n = qlora_act_workspace_bytes_bwd(T, K, N, r)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dy.device)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    g = ActGrad(code, sx, sz, sm, _ptr(dx_add), dx.data_ptr(), _ptr(d_lora_a), _ptr(d_lora_b), _ptr(d_bias),
+                _ptr(d_mul))
     fn = _entry("qlora_linear_act_bwd", ct, qw)
     _check(fn, getattr(lib(), fn)(
-        _ptr(dy), T, K, N, _ptr(qw.codes), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r, float(scaling),
-        ctypes.byref(g), _ptr(workspace), workspace.numel(), _stream()))
-    return ActGrads(**res)
+        dy.data_ptr(), T, K, N, qw.codes.data_ptr(), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r,
+        float(scaling), ctypes.byref(g), workspace.data_ptr(), workspace.numel(), _stream()))
+    return ActGrads(dx, d_lora_a, d_lora_b, d_bias, d_mul)
 
 
 # The _sq entry points under their C names (the wrappers above pick them for an NF4WeightSQ).
