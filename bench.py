@@ -38,7 +38,7 @@ HBM_PEAK = 8.0e12          # bytes/s, published
 MFMA_BF16_PEAK = 2.5e15    # flop/s, dense bf16, published
 # k_fwd's source: the kernel file and the headers it includes
 GEMM_SOURCES = [os.path.join(ROOT, "qlora_linear_layers_amd", "csrc", f)
-                for f in ("gemm.hip", "common.hpp", "grad.hpp", "plan.hpp")]
+                for f in ("gemm.hip", "common.hpp", "grad.hpp", "act.hpp", "plan.hpp")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "k_fwd_llama65b_T2048_traffic.txt")
 COPY_BYTES = 256 << 20     # calibration copy for the HBM byte counters
 
@@ -741,6 +741,39 @@ def storage_bytes_sq(numel):
     return numel // 2 + 4 * (numel // 64)
 
 
+def measure_mlp(api, torch, synth, reps=10):
+    """The gated feed-forward block (mlp.py) of the LLaMA-7B shapes, r = 64: a training
+    forward that keeps 8-bit checkpoints and the backward from them at T = 2048, and the
+    forward of single tokens (T = 1, 8).  HIP events over `reps` passes after two warm-up
+    passes.  Returns {name: microseconds} and the bytes kept per forward."""
+    from qlora_linear_layers_amd.mlp import AdaptedLinear, GatedMlp
+    g = torch.Generator(device="cuda").manual_seed(1)
+    normal = lambda *sh, std=1.0: torch.randn(sh, generator=g, device="cuda").mul_(std).to(torch.bfloat16)
+    by = {l.name: l for l in synth.LLAMA7B}
+    lin = {n: AdaptedLinear(api.nf4_quantize_dq(normal(by[n].N, by[n].K, std=0.02)), normal(by[n].K, 64, std=0.01),
+                            normal(64, by[n].N, std=0.01), 0.25) for n in ("gate", "up", "down")}
+    mlp = GatedMlp(lin["gate"], lin["up"], lin["down"])
+
+    def us(fn):
+        for _ in range(2):
+            fn()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(reps):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        return 1e3 * a.elapsed_time(b) / reps
+    T, D = 2048, by["gate"].K
+    x, res, dy = normal(T, D), normal(T, D), normal(T, D)
+    _, saved = mlp.forward_train(x, res)
+    out = {"forward_train_T2048_us": us(lambda: mlp.forward_train(x, res)),
+           "backward_T2048_us": us(lambda: mlp.backward(dy, saved))}
+    for t in (1, 8):
+        out[f"forward_T{t}_us"] = us(lambda: mlp.forward(x[:t], res[:t]))
+    return out, saved.nbytes()
+
+
 def only_component(name, api, torch, synth, calib, args):
     """One component alone (for kernel traces and counter runs)."""
     layers7, r, s = synth.TRAIN_7B["layers"], synth.TRAIN_7B["r"], synth.TRAIN_7B["scaling"]
@@ -781,6 +814,9 @@ def only_component(name, api, torch, synth, calib, args):
                                    .to(torch.bfloat16)) for l in layers7]
         secs, nbytes = measure_merge(api, torch, layers7, weight_copies(api, qws), r, s)
         return {"GB/s": round(nbytes / secs / 1e9, 1), "us_per_layer_set": round(1e6 * secs, 2)}
+    if name == "mlp_7b":
+        res, kept = measure_mlp(api, torch, synth)
+        return {**{k: round(v, 2) for k, v in res.items()}, "checkpoint_bytes_T2048": kept}
     if name == "calibration":
         return {k: round(v / 1e9, 1) for k, v in measure_calibration(torch, calib).items()}
     secs, moved, packed, params = measure_stream_70b(torch, synth)
@@ -798,7 +834,7 @@ def main():
                     help="only the headline step and the roofline kernel (for a kernel trace of the step alone)")
     ap.add_argument("--only", choices=("decode", "decode_single", "decode_all7", "decode_valu", "decode_all7_valu",
                                        "decode_mfma", "decode_all7_mfma", "single_layer", "train_7b", "train_7b_fused", "forward_midt", "train_midt",
-                                       "merge", "calibration", "stream_70b"),
+                                       "merge", "mlp_7b", "calibration", "stream_70b"),
                     help="run one component alone (no step, roofline loop or CPU baseline), e.g. for a kernel trace")
     ap.add_argument("--roofline-only", action="store_true",
                     help="only the calibration copy and the k_fwd launches at the 65B shapes (for counter runs)")

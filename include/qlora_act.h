@@ -30,7 +30,7 @@ extern "C" {
  * act8_quantize / act8_dequantize - an activation held in 8 bits.
  *   Blocks are 64 consecutive values (row-major; the last may be shorter).
  *   With c = max|x| of a block:
- *     d = fl32(c / 127),  q = x fl32(127 / c) rounded once to an integer, ties to even,
+ *     d = fl32(c / 127),  q = fl32(x fl32(127 / c)) rounded to an integer, ties to even,
  *   and the block stands for q d: x_out = RNE_16(fl32(q d)).  |x_out - x| is at
  *   most d / 2 and the final roundings.  A block with c < 2^-120 is stored as
  *   zeros; one that holds an inf or NaN has d = NaN and reads back as NaN.

@@ -3,7 +3,7 @@ epilogue forward, its backward, and the 8-bit activation checkpoint.
 
 Activation checkpoint (blocks of 64 consecutive values, the last may be
 shorter): with c the largest magnitude of a block, d = fl32(c / 127) and
-q = x fl32(127 / c) rounded once to an integer, ties to even; the block stands
+q = fl32(x fl32(127 / c)) rounded to an integer, ties to even; the block stands
 for q d.  Blocks with c < 2^-120 are zeros, blocks with an inf or NaN get d = NaN.
 """
 import numpy as np
@@ -61,7 +61,7 @@ def ck_quantize(x):
     safe = np.where(zero, np.float32(1.0), c)
     d = np.where(zero, np.float32(0.0), c / np.float32(127.0)).astype(np.float32)
     inv = np.where(zero, np.float32(0.0), np.float32(127.0) / safe).astype(np.float32)
-    q = np.rint(np.where(bad[:, None], 0.0, blk) * inv.astype(np.float64)[:, None])
+    q = np.rint(np.where(bad[:, None], 0.0, blk).astype(np.float32) * inv[:, None])
     d[bad] = np.nan
     return q.astype(np.int8).reshape(-1)[:n], d
 

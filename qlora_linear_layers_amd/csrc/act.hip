@@ -136,13 +136,21 @@ struct SavedBuf {
 }  // namespace
 
 // A workgroup owns 128 columns (16 lanes of 8) and one range of rows, 16 row
-// slots of four rows each per step: the loads of a step's four rows are all
-// issued before the first is used.  Column sums stay in registers over the
-// steps; the 16 row slots of a column are then added in LDS in slot order, so
-// d_bias is deterministic.
+// slots of two rows each per step: the loads of a step's rows are all issued
+// before the first is used.  Column sums stay in registers over the steps; the
+// 16 row slots of a column are then added in LDS in slot order, so d_bias is
+// deterministic.  dmul, which nothing here reads again, is stored past the
+// caches.
+//
+// Bound by HBM with the VALU close behind (about 25 instruction slots per
+// element for silu, exp and the reciprocal counting four each): 2048 x 11008
+// with Z and mul as checkpoints, 183 MB, takes 38 us (4.8 TB/s).  Forming
+// s dZ B^T in the same pass was slower: the registers of its fragments leave
+// two workgroups a CU, too few to cover the memory latency (80 us for both
+// against 41 + 21).
 template <int ACT, bool F16>
 QL_DEV void act_bwd_block(const ActBwd& a, int bid, float* red) {
-    constexpr int U = 4;
+    constexpr int U = 2;
     const int cb = (int)ceil_div(a.N, 128);
     const int bx = bid % cb, by = bid / cb;
     const int cl = threadIdx.x & 15, slot = threadIdx.x >> 4;
@@ -184,10 +192,13 @@ QL_DEV void act_bwd_block(const ActBwd& a, int bid, float* red) {
                 h[e] *= dy[e];
                 if (has_mul) dy[e] *= m[e];
                 dy[e] *= d;
-                sum[e] += dy[e];
+            }
+            if (a.part) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += dy[e];
             }
             if (ok) {
-                if (a.dmul) *reinterpret_cast<u32x4_t*>(a.dmul + t * a.N + n) = pack8<F16>(h);
+                if (a.dmul) __builtin_nontemporal_store(pack8<F16>(h), reinterpret_cast<u32x4_t*>(a.dmul + t * a.N + n));
                 if (a.dz) *reinterpret_cast<u32x4_t*>(a.dz + t * a.N + n) = pack8<F16>(dy);
             }
         }

@@ -2,7 +2,7 @@
 // by the kernels that end a projection (gemm.hip, gemv.hip) and by act.hip.
 //
 // Activation functions and their slopes (p = act(z) / z for the last three):
-//   silu       p = 1 / (1 + e^-z)                      act' = p (1 + z (1 - p))
+//   silu       p = 1 / (1 + e^-z)                      act' = p + z p (1 - p)
 //   gelu       p = Phi(z) = erfc(-z / sqrt 2) / 2      act' = p + z e^(-z^2/2) / sqrt(2 pi)
 //   gelu_tanh  p = 1 / (1 + e^(-2u)),  u = sqrt(2/pi) (z + 0.044715 z^3)
 //                                                      act' = p + z p (1 - p) 2 u'
@@ -67,7 +67,7 @@ QL_DEV void act_slope(float z, float& v, float& d) {
     } else if constexpr (ACT == kActSilu) {
         const float p = logistic(z);
         v = z * p;
-        d = p * fmaf(z, 1.0f - p, 1.0f);
+        d = fmaf(-v, p, v + p);                              // p + v (1 - p)
     } else if constexpr (ACT == kActGelu) {
         float e;
         const float p = normal_cdf(z, e);
@@ -111,10 +111,12 @@ QL_DEV void act_values(int act, float (&v)[N]) {
 // ------------------------------------------------------------------ 8-bit checkpoints
 //
 // Blocks of 64 consecutive values (row-major).  With c = max|x| of a block:
-//   d = fl32(c / 127),  q = x fl32(127 / c) rounded once to an integer (ties to even),
-// and the block stands for q d.  The scale is divided exactly (IEEE); the code
-// is one fma against 1.5 * 2^23, whose ulp is 1, so its low byte is q in two's
-// complement.  |x| <= c keeps |q| <= 127.  A block whose c is below 2^-120
+//   d = fl32(c / 127),  q = fl32(x fl32(127 / c)) rounded to an integer, ties to even,
+// and the block stands for q d.  The scale and the factor are divided exactly
+// (IEEE).  Rounding the product to fp32 first puts the exact ties of 127 x / c
+// (c a multiple of 127 units) back on the tie, which an fma would miss by the
+// factor's rounding; adding 1.5 * 2^23, whose ulp is 1, then leaves q in two's
+// complement in the low byte.  |x| <= c keeps |q| <= 127.  A block whose c is below 2^-120
 // (where 127 / c leaves the fp32 range) is stored as zeros (d = 0), and one
 // that holds an inf or a NaN gets d = NaN, so it reads back as NaN and an
 // overflow is not lost in the checkpoint.
@@ -148,8 +150,12 @@ QL_DEV uint32_t max_of_8_lanes(uint32_t m) {
     return m;
 }
 
-// fp32 whose low byte is the code of x
-QL_DEV uint32_t ck_code(float x, float inv) { return __float_as_uint(fmaf(x, inv, 12582912.0f)); }
+// fp32 whose low byte is the code of x (two roundings: not to be contracted)
+QL_DEV uint32_t ck_code(float x, float inv) {
+#pragma clang fp contract(off)
+    const float n = x * inv;
+    return __float_as_uint(n + 12582912.0f);
+}
 
 // codes of four values (two packed pairs), value 0 in the low byte
 template <bool F16>

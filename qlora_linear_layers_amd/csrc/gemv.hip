@@ -471,11 +471,10 @@ __global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Code
 
 // Launch 2.  Y[t][n] = sum_ks part[ks][t][n] + sum_j u[t][j] B[j][n] with
 // u = s X A rebuilt from its slice partials, rounded to the 16-bit type.  A
-// workgroup owns 128 columns up to T = 8 (two adjacent ones per lane: N is a
-// multiple of 64, so B is read as dwords, the base partials as float2s and Y
-// written as dwords) and 64 above, and has W waves (T of them up to
-// T = 4, then 4, and 8 for T > 8) that work alone: wave w takes the tokens
-// t = w and, for T > 4, t = w + W (TW of them), adds their base partials in ks
+// workgroup owns 128 columns (two adjacent ones per lane: N is a multiple of 64,
+// so B is read as dwords, the base partials as float2s and Y written as dwords)
+// or 64, and has W waves that work alone: wave w takes the tokens t = w and, with
+// TW = 2, t = w + W (TW of them; see the launcher for W), adds their base partials in ks
 // order, rebuilds each 64-rank chunk of u from the slice
 // partials (lane (g, i) adds ranks 4i .. 4i + 3 over the slices g, g + 4, ...
 // in order, then the four lane groups are added pairwise), and forms the rank
@@ -484,8 +483,12 @@ __global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Code
 // the first slice partials are all issued before the first sum, so for the
 // decode shapes the kernel waits for one round of loads.
 // CPL columns per lane: 2 up to T = 8, 1 above (more workgroups for the
-// 8-wave, 16-token case)
-constexpr int fin_cols(int64_t T) { return T <= 8 ? 128 : 64; }
+// 8-wave, 16-token case), and 1 with one token per wave where the launch has at
+// most 8192 columns, whose 128-column workgroups would be 64 at most (T = 7 on
+// 11008 -> 4096: 21.2 us the launch pair with two columns, 19.8 with one; T = 8
+// on 4096 -> 11008 the same either way, on 8192 -> 22016 44.1 against 46.9).
+constexpr bool fin_wide(int64_t T, int64_t columns) { return T <= 8 && columns > 8192; }
+constexpr int fin_cols(bool wide) { return wide ? 128 : 64; }
 //
 // EPI: Y leaves through the epilogue of its problem, whose operands (bias, mul,
 // residual) are loaded with the partials; a 64-column block of a checkpoint of
@@ -748,6 +751,9 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     GemvGroup g{};
     g.count = count;
     int nl = 0, nbase = 0, nfin = 0;
+    int64_t columns = 0;
+    for (int i = 0; i < count; ++i) columns += probs[i].N;
+    const bool wide = fin_wide(T, columns);
     for (int i = 0; i < count; ++i) {
         const GemvProblem& q = probs[i];
         GemvArgs& a = g.p[i];
@@ -760,7 +766,7 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
         nl += r ? (int)(r_pad / 64) * a.KL : 0;
         g.lora_end[i] = nl;
         nbase += a.gemv_blocks;
-        nfin += (int)ceil_div(q.N, fin_cols(T));
+        nfin += (int)ceil_div(q.N, fin_cols(wide));
         g.fin_end[i] = nfin;
     }
     for (int i = 0; i < count; ++i) g.base_end[i] = (i ? g.base_end[i - 1] : nl) + g.p[i].gemv_blocks;
@@ -814,9 +820,9 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     if (ae != hipSuccess) return ae;
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // waves: one per token up to 4, four for T <= 8 (two tokens each), eight
-    // for T > 8 (two tokens each); every wave loads the B column itself
-    const int fw = T <= 4 ? (int)T : T <= 8 ? 4 : 8;
+    // waves: one per token up to 4 (8 with one column per lane), four for T <= 8
+    // and eight for T > 8 (two tokens each); every wave loads the B column itself
+    const int fw = T <= 4 || (!wide && T <= 8) ? (int)T : T <= 8 ? 4 : 8;
     const dim3 fg((unsigned)nfin), fb((unsigned)(64 * fw));
     auto fin_epi = [&](auto tw, auto cpl, auto epi, const auto& eg) {
         constexpr int TW = decltype(tw)::value, CPL = decltype(cpl)::value;
@@ -838,8 +844,9 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     };
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
-    if (T <= 4) fin_tw(I1{}, I2{});
-    else if (T <= 8) fin_tw(I2{}, I2{});
+    if (wide && T <= 4) fin_tw(I1{}, I2{});
+    else if (wide) fin_tw(I2{}, I2{});
+    else if (T <= 8) fin_tw(I1{}, I1{});
     else fin_tw(I2{}, I1{});
     return hipGetLastError();
 }
