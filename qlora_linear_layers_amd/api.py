@@ -603,63 +603,87 @@ def _act(name):
     return ACTS[name]
 
 
-@dataclass
 class Act8:
-    """8-bit checkpoint of an activation (device tensors): one code per value, one scale per 64."""
-    codes: torch.Tensor       # int8 [numel]
-    scale: torch.Tensor       # float32 [ceil(numel/64)]
-    shape: tuple              # of the activation
+    """8-bit checkpoint of an activation (device tensors): `codes` int8 [numel], one per value, and
+    `scale` float32 [ceil(numel/64)], one per 64; `shape` is the activation's.  One made by
+    act8_empty holds both in a single allocation, and the two tensors are views made when asked for."""
+    __slots__ = ("shape", "numel", "_codes", "_scale", "_buf")
+
+    def __init__(self, codes, scale, shape):
+        self.shape = tuple(shape)
+        self.numel = math.prod(self.shape)
+        self._codes, self._scale, self._buf = codes, scale, None
 
     @property
-    def numel(self):
-        return math.prod(self.shape)
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self.numel]
+        return self._codes
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            self._scale = self._buf[-4 * -(-self.numel // 64):].view(torch.float32)
+        return self._scale
+
+    @property
+    def device(self):
+        return (self._codes if self._buf is None else self._buf).device
 
     def nbytes(self):
-        return self.codes.numel() + 4 * self.scale.numel()
+        return self.numel + 4 * -(-self.numel // 64)
 
+    def check(self, name):
+        """The tensors must hold exactly what the shape needs (an act8_empty's do)."""
+        if self._buf is None:
+            _count(self._codes, self.numel, name + " codes")
+            _count(self._scale, -(-self.numel // 64), name + " scale")
 
-def _check_act8(a8, name):
-    """The checkpoint's tensors must hold exactly what its shape needs."""
-    n = math.prod(a8.shape)
-    _count(a8.codes, n, name + " codes")
-    _count(a8.scale, -(-n // 64), name + " scale")
+    def pointers(self, name):
+        """(codes, scale) addresses of a checkpoint on the GPU."""
+        if self._buf is not None:
+            if not self._buf.is_cuda:
+                raise ValueError(f"{name} codes must be a GPU tensor")
+            p = self._buf.data_ptr()
+            return p, p + -(-self.numel // 16) * 16
+        _dev(self._codes, torch.int8, name + " codes")
+        _dev(self._scale, torch.float32, name + " scale")
+        return self._codes.data_ptr(), self._scale.data_ptr()
 
 
 def act8_empty(shape, device="cuda"):
     """An Act8 of uninitialised storage for an activation of `shape`."""
-    n = math.prod(shape)
-    return Act8(torch.empty(n, dtype=torch.int8, device=device),
-                torch.empty(-(-n // 64), dtype=torch.float32, device=device), tuple(shape))
+    a8 = Act8(None, None, shape)
+    n = a8.numel
+    # codes, rounded up to 16 bytes, then the scales
+    a8._buf = torch.empty(-(-n // 16) * 16 + 4 * -(-n // 64), dtype=torch.int8, device=device)
+    return a8
 
 
 def act8_quantize(x, out=None):
     """bf16 or fp16 activation of any shape -> Act8 (written into `out` if given)."""
     fn = "act8_quantize" + _ct(x, "x")
     if out is not None:
-        _check_act8(out, "out")
+        out.check("out")
         _shape(x, out.shape, "x")
-        _dev(x, x.dtype, "x")
-        _dev(out.codes, torch.int8, "out codes")
-        _dev(out.scale, torch.float32, "out scale")
-    else:
-        _dev(x, x.dtype, "x")
+    _dev(x, x.dtype, "x")
+    if out is None:
         out = act8_empty(x.shape, x.device)
-    _check(fn, getattr(lib(), fn)(x.data_ptr(), x.numel(), out.codes.data_ptr(), out.scale.data_ptr(), _stream()))
+    codes, scale = out.pointers("out")
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), out.numel, codes, scale, _stream()))
     return out
 
 
 def act8_dequantize(a8, dtype=torch.bfloat16, out=None):
     """Act8 -> the 16-bit values it stands for, in `dtype` (or in the dtype of `out`)."""
-    _check_act8(a8, "checkpoint")
-    codes, scale = a8.codes, a8.scale
+    a8.check("checkpoint")
     _shape(out, a8.shape, "out")
-    _dev(codes, torch.int8, "codes")
-    _dev(scale, torch.float32, "scale")
+    codes, scale = a8.pointers("checkpoint")
     if out is None:
-        out = torch.empty(a8.shape, dtype=dtype, device=codes.device)
+        out = torch.empty(a8.shape, dtype=dtype, device=a8.device)
     fn = "act8_dequantize" + _ct(out, "out")
     _dev(out, out.dtype, "out")
-    _check(fn, getattr(lib(), fn)(codes.data_ptr(), scale.data_ptr(), codes.numel(), out.data_ptr(), _stream()))
+    _check(fn, getattr(lib(), fn)(codes, scale, a8.numel, out.data_ptr(), _stream()))
     return out
 
 
@@ -687,8 +711,8 @@ def qlora_linear_act_fwd(x, qw, lora_a=None, lora_b=None, scaling=1.0, bias=None
     _shape(out, (T, N), "out")
     if z is not None:
         if save == "z8":
-            _check_act8(z, "z")
-        if tuple(z.shape) != (T, N):
+            z.check("z")
+        if z.shape != (T, N):
             raise ValueError(f"z has shape {tuple(z.shape)}, expected {(T, N)}")
     dt = x.dtype
     _dev(x, dt, "x")
@@ -704,9 +728,7 @@ def qlora_linear_act_fwd(x, qw, lora_a=None, lora_b=None, scaling=1.0, bias=None
     if save == "z8":
         if z is None:
             z = act8_empty((T, N), x.device)
-        _dev(z.codes, torch.int8, "z codes")
-        _dev(z.scale, torch.float32, "z scale")
-        zc, zs = z.codes.data_ptr(), z.scale.data_ptr()
+        zc, zs = z.pointers("z")
     elif save:
         if z is None:
             z = torch.empty_like(out)
@@ -742,9 +764,9 @@ _ABSENT = Saved()
 def _saved(v, shape, name):
     """Checks of one saved activation (tensor, Act8 or None) against its shape."""
     if isinstance(v, Act8):
-        _check_act8(v, name)
-        if tuple(v.shape) != shape:
-            raise ValueError(f"{name} has shape {tuple(v.shape)}, expected {shape}")
+        v.check(name)
+        if v.shape != shape:
+            raise ValueError(f"{name} has shape {v.shape}, expected {shape}")
     else:
         _shape(v, shape, name)
 
@@ -754,9 +776,7 @@ def _saved_arg(v, dtype, name):
     if v is None:
         return _ABSENT
     if isinstance(v, Act8):
-        _dev(v.codes, torch.int8, name + " codes")
-        _dev(v.scale, torch.float32, name + " scale")
-        return Saved(None, v.codes.data_ptr(), v.scale.data_ptr())
+        return Saved(None, *v.pointers(name))
     _dev(v, dtype, name)
     return Saved(v.data_ptr(), None, None)
 
