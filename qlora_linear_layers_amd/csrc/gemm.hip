@@ -167,9 +167,10 @@ QL_DEV void otile_put4(lds8_t* lo, const f32x16_t& v, int g, int t, int col) {
 }
 
 // tile[t][c] = src[t0 + t][c0 + c] where that exists, 0 elsewhere (C % 8 == 0)
+template <int TT>
 QL_DEV void otile_load(lds8_t* lo, const uint16_t* src, int64_t lds, int64_t t0, int64_t c0, int64_t T, int64_t C) {
 #pragma unroll 8
-    for (int it = 0; it < 256 * 32 / kThreads; ++it) {
+    for (int it = 0; it < TT * 32 / kThreads; ++it) {
         const int u = threadIdx.x + it * kThreads;
         const int t = u >> 5, c = u & 31;
         const int64_t tg = t0 + t, cg = c0 + c * 8;
@@ -181,9 +182,10 @@ QL_DEV void otile_load(lds8_t* lo, const uint16_t* src, int64_t lds, int64_t t0,
 
 // out[t0 + t][c0 + c] = tile[t][c] for t0 + t < T and c0 + c < C (C % 8 == 0):
 // each wave store covers two rows of 512 contiguous bytes.
+template <int TT>
 QL_DEV void otile_store(const lds8_t* lo, uint16_t* out, int64_t ldo, int64_t t0, int64_t c0, int64_t T, int64_t C) {
 #pragma unroll 8
-    for (int it = 0; it < 256 * 32 / kThreads; ++it) {
+    for (int it = 0; it < TT * 32 / kThreads; ++it) {
         const int u = threadIdx.x + it * kThreads;
         const int t = u >> 5, c = u & 31;
         const int64_t tg = t0 + t, cg = c0 + c * 8;
@@ -224,6 +226,7 @@ struct FwdArgs {
     int64_t T, K, N, r, r_pad;
     float* part;              // split-k: fp32 partial tiles [splits][N][T rounded up to 4]
     int splits;
+    int na1;                  // tile mix: row tiles of W under 256-token tiles
 };
 
 // Y = X W'^T (+ (s X A) B), tile 256 (n) x 256 (t), waves stacked along n.
@@ -243,17 +246,21 @@ struct FwdArgs {
 //
 // SQ: single quantization, the block constant is the stored fp32 absmax (one
 // 4-byte load per row and tile instead of the FP8 code and the super-scale).
-template <bool SQ>
+//
+// TT: tokens of the tile, 256, or 192 or 128 in the last round of a launch whose
+// 256-token tiles would leave CUs idle there (see tile_mix).
+template <bool SQ, int TT_>
 struct FwdPipe {
-    static constexpr int TT = 256;
-    static constexpr uint32_t kTile = TT * 128;   // one [256][64] bf16 LDS tile
+    static constexpr int TT = TT_;
+    static constexpr int NB = TT / 32;            // 32-token B fragments, and 16-byte X chunks per thread
+    static constexpr uint32_t kTile = 256 * 128;  // LDS of one [TT][64] bf16 tile
     rsrc_t rc, rf, rs, rx;
-    uint32_t cvo[2], fvo[2], blk[2], xvo[8];
+    uint32_t cvo[2], fvo[2], blk[2], xvo[NB];
     bool wok[2];
     uint32_t lane8;
     int KT;
     // global-load register sets, indexed by tile parity
-    u32x4_t xr[2][8];
+    u32x4_t xr[2][NB];
     u32x4_t wc[2][2];
     uint32_t wf[2][2];
     float ws[2][2];
@@ -277,11 +284,11 @@ struct FwdPipe {
     QL_DEV void load_x(int kt, int par) {
         kt = kt < KT ? kt : KT - 1;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) xr[par][c] = bload16(rx, xvo[c], (uint32_t)kt * 128u);
+        for (int c = 0; c < NB; ++c) xr[par][c] = bload16(rx, xvo[c], (uint32_t)kt * 128u);
     }
     QL_DEV void store_x(int par, lds8_t* lx) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < NB; ++c) {
             const int ch = threadIdx.x + c * kThreads;
             *reinterpret_cast<lds_u32x4_t*>(lx + lds_off(ch >> 3, ch & 7)) = xr[par][c];
         }
@@ -291,13 +298,15 @@ struct FwdPipe {
 // Pieces of one MFMA step s (16 k): eight X fragments from LDS, the eight
 // codebook pairs of the two A fragments (codes dword s of each W row), the
 // A fragments themselves, and the sixteen MFMAs.
-typedef bf16x8_t XFr[8];
+template <int NB>
+using XFr = bf16x8_t[NB];
 typedef f32x2_t QPr[2][4];
 typedef bf16x8_t AFr[2];
 
-QL_DEV void read_x(XFr& x, const lds8_t* xb, int s, int r, int h) {
+template <int NB>
+QL_DEV void read_x(XFr<NB>& x, const lds8_t* xb, int s, int r, int h) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = lds_frag(xb, 32 * j + r, 4 * h + s);
+    for (int j = 0; j < NB; ++j) x[j] = lds_frag(xb, 32 * j + r, 4 * h + s);
 }
 
 QL_DEV void read_q(QPr& q, const u32x4_t (&wc)[2], int s, uint32_t lane8) {
@@ -322,10 +331,10 @@ QL_DEV void make_a(AFr& a, const QPr& q, const float (&c1p)[2]) {
     }
 }
 
-template <bool F16>
-QL_DEV void mfma16(f32x16_t (&acc)[2][8], const AFr& a, const XFr& x) {
+template <bool F16, int NB>
+QL_DEV void mfma16(f32x16_t (&acc)[2][NB], const AFr& a, const XFr<NB>& x) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < NB; ++j) {
         acc[0][j] = mfma32x32x16<F16>(a[0], x[j], acc[0][j]);
         acc[1][j] = mfma32x32x16<F16>(a[1], x[j], acc[1][j]);
     }
@@ -351,63 +360,65 @@ QL_DEV void interleave() {
 // the codebook pairs of step s+2 are read, and the A fragments of step s+1
 // are built from pairs read during step s-1.  On entry xa / aa hold step 0 of
 // tile kt and qa the pairs of step 1; on exit the same for tile kt+1.
-template <int P, bool SQ, bool F16>
-QL_DEV void fwd_tile(FwdPipe<SQ>& pp, int kt, f32x16_t (&acc)[2][8], lds8_t* lX, int r, int h, XFr& xa, AFr& aa,
-                     QPr& qa, float (&c1p)[2]) {
+template <int P, bool SQ, bool F16, int TT>
+QL_DEV void fwd_tile(FwdPipe<SQ, TT>& pp, int kt, f32x16_t (&acc)[2][TT / 32], lds8_t* lX, int r, int h,
+                     XFr<TT / 32>& xa, AFr& aa, QPr& qa, float (&c1p)[2]) {
     constexpr int Q = P ^ 1;
-    const lds8_t* xb = lX + P * FwdPipe<SQ>::kTile;
-    XFr xb_;
+    constexpr int NB = TT / 32, NM = 2 * NB, NV = NB == 8 ? 2 : NB == 6 ? 3 : 4;   // MFMAs of a step, VALU per MFMA
+    constexpr uint32_t kTile = FwdPipe<SQ, TT>::kTile;
+    const lds8_t* xb = lX + P * kTile;
+    XFr<NB> xb_;
     AFr ab;
     QPr qb;
     pp.load_x(kt + 2, P);                     // staging set P held tile kt, stored during tile kt-1
     __builtin_amdgcn_sched_barrier(0);
     // step 0
-    read_x(xb_, xb, 1, r, h);
+    read_x<NB>(xb_, xb, 1, r, h);
     read_q(qb, pp.wc[P], 2, pp.lane8);
     make_a<F16>(ab, qa, c1p);
-    mfma16<F16>(acc, aa, xa);
-    interleave<16, 16, 16>();
+    mfma16<F16, NB>(acc, aa, xa);
+    interleave<NM, NM, NM, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     // step 1
-    read_x(xa, xb, 2, r, h);
+    read_x<NB>(xa, xb, 2, r, h);
     read_q(qa, pp.wc[P], 3, pp.lane8);
     make_a<F16>(aa, qb, c1p);
-    mfma16<F16>(acc, ab, xb_);
-    interleave<16, 16, 16>();
+    mfma16<F16, NB>(acc, ab, xb_);
+    interleave<NM, NM, NM, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     // step 2: the pairs of the next tile's step 0 come from code set Q
-    read_x(xb_, xb, 3, r, h);
+    read_x<NB>(xb_, xb, 3, r, h);
     read_q(qb, pp.wc[Q], 0, pp.lane8);
     make_a<F16>(ab, qa, c1p);
-    mfma16<F16>(acc, aa, xa);
-    interleave<16, 16, 16>();
+    mfma16<F16, NB>(acc, aa, xa);
+    interleave<NM, NM, NM, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     pp.load_w(kt + 2, P);                     // code set P is no longer read
     const float n1p[2] = {pp.c1(Q, 0), pp.c1(Q, 1)};
     // step 3: the first half of its MFMAs cover the X store and the barrier
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NB / 2; ++j) {
         acc[0][j] = mfma32x32x16<F16>(ab[0], xb_[j], acc[0][j]);
         acc[1][j] = mfma32x32x16<F16>(ab[1], xb_[j], acc[1][j]);
     }
-    pp.store_x(Q, lX + Q * FwdPipe<SQ>::kTile);
+    pp.store_x(Q, lX + Q * kTile);
     __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
-    read_x(xa, lX + Q * FwdPipe<SQ>::kTile, 0, r, h);
+    read_x<NB>(xa, lX + Q * kTile, 0, r, h);
     read_q(qa, pp.wc[Q], 1, pp.lane8);
     make_a<F16>(aa, qb, n1p);
 #pragma unroll
-    for (int j = 4; j < 8; ++j) {
+    for (int j = NB / 2; j < NB; ++j) {
         acc[0][j] = mfma32x32x16<F16>(ab[0], xb_[j], acc[0][j]);
         acc[1][j] = mfma32x32x16<F16>(ab[1], xb_[j], acc[1][j]);
     }
-    interleave<8, 8, 8>();
+    interleave<NM - 2 * (NB / 2), 8, 8, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     c1p[0] = n1p[0];
     c1p[1] = n1p[1];
 }
 
-// The epilogue's operands of one 256 x 256 tile: lane l takes columns
+// The epilogue's operands of one 256-column tile: lane l takes columns
 // 8 (l % 32) .. +7 of row l / 32 + 8 i of each 128-row half, sixteen rows in
 // groups of kGrp, one group ahead of the rows in work (two register sets).
 // An absent operand has an empty buffer and reads zeros without a memory
@@ -416,18 +427,18 @@ struct EpiPipe {
     static constexpr int kGrp = 4, kGroups = 16 / kGrp;
     rsrc_t rm, rr;
     uint32_t off0;
-    int64_t row2, left;                       // bytes of a row; rows from the tile's first to the last
+    int64_t row2, left;                       // bytes of a row; rows of the tile that exist
     u32x4_t bq, mq[2][kGrp], rq[2][kGrp];
 
     static QL_DEV int row(int q, int u) { return (int)(threadIdx.x >> 5) + 8 * (q * kGrp + u); }
-    QL_DEV void init(const Epilogue& ep, int64_t T, int64_t N, int64_t t0, int64_t n0) {
+    QL_DEV void init(const Epilogue& ep, int64_t T, int64_t N, int64_t t0, int64_t n0, int TT) {
         const int64_t n = n0 + (threadIdx.x & 31) * 8;
         rm = make_rsrc(ep.mul, ep.mul ? T * N * 2 : 0);
         rr = make_rsrc(ep.res, ep.res ? T * N * 2 : 0);
         bq = bload16(make_rsrc(ep.bias, ep.bias ? N * 2 : 0), n < N ? (uint32_t)(n * 2) : kOOB, 0);
         row2 = N * 2;
         off0 = (uint32_t)((t0 * N + n) * 2);
-        left = n < N ? T - t0 : 0;
+        left = n < N ? (T - t0 < TT ? T - t0 : TT) : 0;
     }
     QL_DEV void load(int hf, int q, int slot) {
 #pragma unroll
@@ -449,33 +460,20 @@ struct EpiPipe {
 //
 // EPI: the tile ends in the epilogue `ep` instead of the plain rounding (a
 // split tile's epilogue runs in k_split_sum).
-template <bool SQ, bool F16, bool SPLIT, bool EPI>
-__global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epilogue ep) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+template <bool SQ, bool F16, bool SPLIT, bool EPI, int TT>
+QL_DEV void fwd_block(const FwdArgs& p, const Epilogue& ep, uint8_t* smem_raw, int ta, int tb, int split, int kt0,
+                      int kt1) {
     lds8_t* smem = (lds8_t*)(smem_raw);
-    constexpr int TT = FwdPipe<SQ>::TT;
-    constexpr uint32_t kTile = FwdPipe<SQ>::kTile;
+    constexpr int NB = TT / 32;
+    constexpr uint32_t kTile = FwdPipe<SQ, TT>::kTile;
     lds8_t* const lX = smem;                  // 2 tiles (the LoRA phase reuses them)
     lds8_t* const lL = smem + kTile;
     lds8_t* const tbl = smem + 2 * kTile;     // wide pair table
-    build_wide_pair_table(tbl, cb);
-
-    const int ga = (int)ceil_div(p.N, 256), gb = (int)ceil_div(p.T, TT);
-    const int KT_all = (int)(p.K / 64);
-    int ta, tb, split = 0, kt0 = 0, kt1 = KT_all;
-    if constexpr (SPLIT) {
-        split = (int)blockIdx.x / (ga * gb);
-        tile_of((int)blockIdx.x % (ga * gb), ga, gb, ta, tb);
-        kt0 = split * KT_all / p.splits;
-        kt1 = (split + 1) * KT_all / p.splits;
-    } else {
-        tile_of(blockIdx.x, ga, gb, ta, tb);
-    }
     const int64_t n0 = (int64_t)ta * 256, t0 = (int64_t)tb * TT;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int r = lane & 31, h = lane >> 5;
 
-    FwdPipe<SQ> pp;
+    FwdPipe<SQ, TT> pp;
     pp.rc = make_rsrc(p.codes, p.N * p.K / 2);
     if constexpr (SQ) {
         pp.rf = make_rsrc(p.absmax, p.N * p.K / 64 * 4);
@@ -496,17 +494,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
         pp.blk[i] = pp.wok[i] ? (uint32_t)(n * (p.K / 64) + kt0) : 0u;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < NB; ++c) {
         const int ch = threadIdx.x + c * kThreads;
         const int64_t t = t0 + (ch >> 3);
         pp.xvo[c] = t < p.T ? (uint32_t)((t * p.K + (int64_t)kt0 * 64 + (ch & 7) * 8) * 2) : kOOB;
     }
 
-    f32x16_t acc[2][8];
+    f32x16_t acc[2][NB];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
@@ -517,7 +515,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
     pp.load_x(1, 1);
     pp.store_x(0, lX);
     __syncthreads();                          // pair table and X tile 0 visible
-    XFr xa;
+    XFr<NB> xa;
     AFr aa;
     QPr qa;
     float c1p[2] = {pp.c1(0, 0), pp.c1(0, 1)};
@@ -526,19 +524,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
         read_q(q0, pp.wc[0], 0, pp.lane8);
         make_a<F16>(aa, q0, c1p);
         read_q(qa, pp.wc[0], 1, pp.lane8);
-        read_x(xa, lX, 0, r, h);
+        read_x<NB>(xa, lX, 0, r, h);
     }
     const int KT = pp.KT;
     int kt = 0;
     for (; kt + 1 < KT; kt += 2) {
-        fwd_tile<0, SQ, F16>(pp, kt, acc, lX, r, h, xa, aa, qa, c1p);
-        fwd_tile<1, SQ, F16>(pp, kt + 1, acc, lX, r, h, xa, aa, qa, c1p);
+        fwd_tile<0, SQ, F16, TT>(pp, kt, acc, lX, r, h, xa, aa, qa, c1p);
+        fwd_tile<1, SQ, F16, TT>(pp, kt + 1, acc, lX, r, h, xa, aa, qa, c1p);
     }
-    if (kt < KT) fwd_tile<0, SQ, F16>(pp, kt, acc, lX, r, h, xa, aa, qa, c1p);
+    if (kt < KT) fwd_tile<0, SQ, F16, TT>(pp, kt, acc, lX, r, h, xa, aa, qa, c1p);
 
     [[maybe_unused]] EpiPipe eo;
     if constexpr (EPI) {                      // the first rows' operands arrive during the LoRA term
-        eo.init(ep, p.T, p.N, t0, n0);
+        eo.init(ep, p.T, p.N, t0, n0, TT);
         eo.load(0, 0, 0);
     }
     if (p.r > 0 && split == 0) {
@@ -560,7 +558,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
                 const bf16x8_t a0 = lds_frag(lL, 64 * w + r, 4 * h + s);
                 const bf16x8_t a1 = lds_frag(lL, 64 * w + 32 + r, 4 * h + s);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < NB; ++j) {
                     const bf16x8_t b = lds_frag(lX, 32 * j + r, 4 * h + s);
                     acc[0][j] = mfma32x32x16<F16>(a0, b, acc[0][j]);
                     acc[1][j] = mfma32x32x16<F16>(a1, b, acc[1][j]);
@@ -584,7 +582,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
         for (int i = 0; i < 2; ++i) {                                    // unrolled: acc indices stay static
             __syncthreads();                                             // LDS readers are done
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NB; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -616,12 +614,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
         f32x4_t* lt = reinterpret_cast<f32x4_t*>(smem_raw);              // [128][64] chunks of 4 columns
         const int64_t n = n0 + (threadIdx.x & 31) * 8;
 #pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < (TT > 128 ? 2 : 1); ++hf) {
             __syncthreads();                                             // LDS readers are done
             auto stage = [&](auto first) {                               // static accumulator indices
                 constexpr int J0 = decltype(first)::value;
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj)
+                for (int jj = 0; jj < (NB - J0 < 4 ? NB - J0 : 4); ++jj)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -631,8 +629,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
                                 f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
                         }
             };
-            if (hf == 0) stage(std::integral_constant<int, 0>{});
-            else stage(std::integral_constant<int, 4>{});
+            if constexpr (NB > 4) {
+                if (hf == 0) stage(std::integral_constant<int, 0>{});
+                else stage(std::integral_constant<int, 4>{});
+            } else {
+                stage(std::integral_constant<int, 0>{});
+            }
             __syncthreads();
             auto rows = [&](int q, int slot) {                           // group q of this half
 #pragma unroll
@@ -641,7 +643,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
                     const int64_t t = t0 + 128 * hf + tl;
                     const f32x4_t a = lt[tl * 64 + (c ^ (tl & 31))], b = lt[tl * 64 + ((c + 1) ^ (tl & 31))];
                     float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-                    if (t < p.T && n < p.N)                              // whole 64-column blocks (N % 64 == 0)
+                    if (128 * hf + tl < eo.left)                         // whole 64-column blocks (N % 64 == 0)
                         epilogue8<F16>(ep, v, eo.bq, eo.mq[slot][u], eo.rq[slot][u], t, n, p.N, p.y);
                 }
             };
@@ -661,11 +663,42 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) otile_put4<F16>(smem, acc[i][j], g, 32 * j + r, 64 * w + 32 * i + 8 * g + 4 * h);
     __syncthreads();
-    otile_store(smem, p.y, p.N, t0, n0, p.T, p.N);
+    otile_store<TT>(smem, p.y, p.N, t0, n0, p.T, p.N);
+}
+
+// TT2 > 0: the grid is a tile mix.  Workgroups [0, n1) take the 256-token tiles
+// of the first na1 row tiles of W, the rest TT2-token tiles of the others (all of
+// them with na1 = 0).  Every output is the same sum in the same order whatever
+// its tile's size, so the bits do not depend on the mix.
+template <bool SQ, bool F16, bool SPLIT, bool EPI, int TT2>
+__global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epilogue ep) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    build_wide_pair_table((lds8_t*)smem_raw + 2 * FwdPipe<SQ, 256>::kTile, cb);
+    const int ga = (int)ceil_div(p.N, 256), gb = (int)ceil_div(p.T, 256);
+    const int KT = (int)(p.K / 64);
+    int ta, tb;
+    if constexpr (SPLIT) {
+        const int split = (int)blockIdx.x / (ga * gb);
+        tile_of((int)blockIdx.x % (ga * gb), ga, gb, ta, tb);
+        fwd_block<SQ, F16, true, EPI, 256>(p, ep, smem_raw, ta, tb, split, split * KT / p.splits,
+                                           (split + 1) * KT / p.splits);
+    } else if constexpr (TT2 == 0) {
+        tile_of((int)blockIdx.x, ga, gb, ta, tb);
+        fwd_block<SQ, F16, false, EPI, 256>(p, ep, smem_raw, ta, tb, 0, 0, KT);
+    } else {
+        const int n1 = p.na1 * gb;
+        if ((int)blockIdx.x < n1) {
+            tile_of((int)blockIdx.x, p.na1, gb, ta, tb);
+            fwd_block<SQ, F16, false, EPI, 256>(p, ep, smem_raw, ta, tb, 0, 0, KT);
+        } else {
+            tile_of((int)blockIdx.x - n1, ga - p.na1, (int)ceil_div(p.T, TT2), ta, tb);
+            fwd_block<SQ, F16, false, EPI, TT2>(p, ep, smem_raw, p.na1 + ta, tb, 0, 0, KT);
+        }
+    }
 }
 
 // out[t][c] = RNE_16(sum_s part[s][c][t]) for the split-k GEMMs: a workgroup
@@ -763,6 +796,7 @@ struct DxArgs {
     int64_t T, K, N, r, r_pad;
     float* part;              // split-k: fp32 partial tiles [splits][K][T rounded up to 4]
     int splits;
+    int na1;                  // tile mix: row tiles of dX^T under 256-token tiles
 };
 
 // The transposed block scales alone (when no other launch of the backward
@@ -801,14 +835,16 @@ QL_DEV uint32_t lds_off_w(int row, int chunk) { return lds_off(row ^ ((row >> 6)
 
 typedef f32x2_t DqPairs[8];   // codebook pairs of one quarter patch: code byte j of rows 0..7
 
+template <int TT>
 struct DxPipe {
+    static constexpr int NX = TT / 32;    // 16-byte dY chunks per thread
     static constexpr uint32_t kTile = 256 * 128;
     rsrc_t rc, rs, rd;
-    uint32_t cvo, svo, dvo[8];
+    uint32_t cvo, svo, dvo[NX];
     uint32_t lane8;
     int64_t K, N;
     int NT;
-    u32x4_t dr[8];                 // dY rows of the next tile to store
+    u32x4_t dr[NX];                // dY rows of the next tile to store
     uint32_t cw[2][8];             // W codes of the tiles being staged, by parity
     u32x4_t sc[2][2];              // their eight block scales (rows n..n+7)
 
@@ -823,11 +859,11 @@ struct DxPipe {
     QL_DEV void load_dy(int kt) {
         kt = kt < NT ? kt : NT - 1;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) dr[c] = bload16(rd, dvo[c], (uint32_t)kt * 128u);
+        for (int c = 0; c < NX; ++c) dr[c] = bload16(rd, dvo[c], (uint32_t)kt * 128u);
     }
     QL_DEV void store_dy(lds8_t* l) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < NX; ++c) {
             const int ch = threadIdx.x + c * kThreads;
             *reinterpret_cast<lds_u32x4_t*>(l + lds_off(ch >> 3, ch & 7)) = dr[c];
         }
@@ -862,83 +898,86 @@ struct DxPipe {
     }
 };
 
+// NJ: 32-token B fragments of a wave (its half of the tile's tokens)
+template <int NJ>
 struct DxFrags {
-    bf16x8_t a[4], b[4];
+    bf16x8_t a[4], b[NJ];
 };
 
-template <bool kMapW>
-QL_DEV void dx_reads(DxFrags& f, const lds8_t* lw, const lds8_t* ld, int s, int wa, int wb, int r, int h) {
+template <bool kMapW, int NJ>
+QL_DEV void dx_reads(DxFrags<NJ>& f, const lds8_t* lw, const lds8_t* ld, int s, int wa, int wb, int r, int h) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = wa * 128 + i * 32 + r;
         f.a[i] = *reinterpret_cast<const lds_bf16x8_t*>(lw + (kMapW ? lds_off_w(row, 2 * s + h) : lds_off(row, 2 * s + h)));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.b[j] = lds_frag(ld, wb * 128 + j * 32 + r, 2 * s + h);
+    for (int j = 0; j < NJ; ++j) f.b[j] = lds_frag(ld, (wb * NJ + j) * 32 + r, 2 * s + h);
 }
 
-template <bool F16>
-QL_DEV void dx_mfma(f32x16_t (&acc)[4][4], const DxFrags& f) {
+template <bool F16, int NJ>
+QL_DEV void dx_mfma(f32x16_t (&acc)[4][NJ], const DxFrags<NJ>& f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
             acc[i][j] = mfma32x32x16<F16>(f.a[i], f.b[j], acc[i][j]);
 }
 
 // MFMAs of output rows i in [i0, i1) only (used to split a step around the barrier)
-template <int i0, int i1, bool F16>
-QL_DEV void dx_mfma_rows(f32x16_t (&acc)[4][4], const DxFrags& f) {
+template <int i0, int i1, bool F16, int NJ>
+QL_DEV void dx_mfma_rows(f32x16_t (&acc)[4][NJ], const DxFrags<NJ>& f) {
 #pragma unroll
     for (int i = i0; i < i1; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
             acc[i][j] = mfma32x32x16<F16>(f.a[i], f.b[j], acc[i][j]);
 }
 
-template <int P, bool F16>
-QL_DEV void dx_tile(DxPipe& pp, int kt, f32x16_t (&acc)[4][4], lds8_t* lW, lds8_t* lD, int wa, int wb, int r,
-                    int h, DxFrags& f0, DqPairs& qa) {
+template <int P, bool F16, int TT>
+QL_DEV void dx_tile(DxPipe<TT>& pp, int kt, f32x16_t (&acc)[4][TT / 64], lds8_t* lW, lds8_t* lD, int wa, int wb, int r,
+                    int h, DxFrags<TT / 64>& f0, DqPairs& qa) {
     constexpr int Q = P ^ 1;
-    const lds8_t* cw = lW + P * DxPipe::kTile;
-    const lds8_t* cd = lD + P * DxPipe::kTile;
-    lds8_t* nw = lW + Q * DxPipe::kTile;
-    lds8_t* nd = lD + Q * DxPipe::kTile;
-    DxFrags f1;
+    constexpr int NJ = TT / 64, NM = 4 * NJ, NV = NJ == 4 ? 2 : NJ == 3 ? 3 : 4;   // MFMAs of a step, VALU per MFMA
+    const lds8_t* cw = lW + P * DxPipe<TT>::kTile;
+    const lds8_t* cd = lD + P * DxPipe<TT>::kTile;
+    lds8_t* nw = lW + Q * DxPipe<TT>::kTile;
+    lds8_t* nd = lD + Q * DxPipe<TT>::kTile;
+    DxFrags<NJ> f1;
     DqPairs qb;
     // step 0
-    dx_reads<true>(f1, cw, cd, 1, wa, wb, r, h);
+    dx_reads<true, NJ>(f1, cw, cd, 1, wa, wb, r, h);
     pp.lookup(qb, Q, 1);
     pp.template finish<F16>(qa, Q, 0, nw);
-    dx_mfma<F16>(acc, f0);
-    interleave<16, 16, 16>();
+    dx_mfma<F16, NJ>(acc, f0);
+    interleave<NM, NM, NM, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     // step 1
-    dx_reads<true>(f0, cw, cd, 2, wa, wb, r, h);
+    dx_reads<true, NJ>(f0, cw, cd, 2, wa, wb, r, h);
     pp.lookup(qa, Q, 2);
     pp.template finish<F16>(qb, Q, 1, nw);
-    dx_mfma<F16>(acc, f1);
-    interleave<16, 16, 16>();
+    dx_mfma<F16, NJ>(acc, f1);
+    interleave<NM, NM, NM, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     // step 2
-    dx_reads<true>(f1, cw, cd, 3, wa, wb, r, h);
+    dx_reads<true, NJ>(f1, cw, cd, 3, wa, wb, r, h);
     pp.lookup(qb, Q, 3);
     pp.template finish<F16>(qa, Q, 2, nw);
-    dx_mfma<F16>(acc, f0);
-    interleave<16, 16, 16>();
+    dx_mfma<F16, NJ>(acc, f0);
+    interleave<NM, NM, NM, 0, NV>();
     __builtin_amdgcn_sched_barrier(0);
     // step 3
-    dx_mfma_rows<0, 2, F16>(acc, f1);
+    dx_mfma_rows<0, 2, F16, NJ>(acc, f1);
     pp.template finish<F16>(qb, Q, 3, nw);
     pp.store_dy(nd);
-    interleave<8, 0, 8, 8, 4>();
+    interleave<NM / 2, 0, NM / 2, NM / 2, 2 * NV>();
     __builtin_amdgcn_sched_barrier(0);
     pp.load_dy(kt + 2);                       // dY registers are free again
     __syncthreads();
-    dx_reads<true>(f0, nw, nd, 0, wa, wb, r, h);
+    dx_reads<true, NJ>(f0, nw, nd, 0, wa, wb, r, h);
     pp.lookup(qa, P, 0);                      // tile kt+2's codes (set P, loaded during tile kt-1)
-    dx_mfma_rows<2, 4, F16>(acc, f1);
-    interleave<8, 16, 0>();
+    dx_mfma_rows<2, 4, F16, NJ>(acc, f1);
+    interleave<NM / 2, NM, 0>();
     __builtin_amdgcn_sched_barrier(0);
     pp.load_w(kt + 3, Q);                     // set Q (tile kt+1) is no longer read
 }
@@ -949,33 +988,20 @@ QL_DEV void dx_tile(DxPipe& pp, int kt, f32x16_t (&acc)[4][4], lds8_t* lW, lds8_
 //
 // ADD: dX += dx_add, in fp32 before the rounding (a split tile's is added by
 // k_split_sum).
-template <bool F16, bool FUSED, bool SPLIT, bool ADD>
-__global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, FusedGrads fz) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+template <bool F16, bool SPLIT, bool ADD, int TT>
+QL_DEV void dx_block(const DxArgs& p, uint8_t* smem_raw, int ta, int tb, int split, int nt0, int nt1) {
     lds8_t* smem = (lds8_t*)(smem_raw);
-    constexpr uint32_t kTile = DxPipe::kTile;
+    constexpr int NJ = TT / 64;
+    constexpr uint32_t kTile = DxPipe<TT>::kTile;
     lds8_t* const lW = smem;                  // 2 tiles [256 k][64 n] (rows permuted)
-    lds8_t* const lD = smem + 2 * kTile;      // 2 tiles [256 t][64 n]
+    lds8_t* const lD = smem + 2 * kTile;      // 2 tiles [TT t][64 n]
     lds8_t* const tbl = smem + 4 * kTile;     // 16-copy pair table
-    build_pair_table16(tbl, cb);
-    const int ga = (int)ceil_div(p.K, 256), gb = (int)ceil_div(p.T, 256);
-    int ta, tb, split = 0;
-    const int NT_all = (int)(p.N / 64);
-    int nt0 = 0, nt1 = NT_all;
-    if constexpr (SPLIT) {
-        split = (int)blockIdx.x / (ga * gb);
-        tile_of((int)blockIdx.x % (ga * gb), ga, gb, ta, tb);
-        nt0 = split * NT_all / p.splits;
-        nt1 = (split + 1) * NT_all / p.splits;
-    } else {
-        tile_of(blockIdx.x, ga, gb, ta, tb);
-    }
-    const int64_t k0 = (int64_t)ta * 256, t0 = (int64_t)tb * 256;
+    const int64_t k0 = (int64_t)ta * 256, t0 = (int64_t)tb * TT;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wa = wave >> 1, wb = wave & 1;
     const int r = lane & 31, h = lane >> 5;
 
-    DxPipe pp;
+    DxPipe<TT> pp;
     pp.K = p.K;
     pp.N = p.N;
     pp.NT = nt1 - nt0;
@@ -992,17 +1018,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
         pp.svo = ok ? (uint32_t)(((k / 64) * p.N + nb) * 4) : kOOB;
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < DxPipe<TT>::NX; ++c) {
         const int ch = threadIdx.x + c * kThreads;
         const int64_t t = t0 + (ch >> 3);
         pp.dvo[c] = t < p.T ? (uint32_t)((t * p.N + (int64_t)nt0 * 64 + (ch & 7) * 8) * 2) : kOOB;
     }
 
-    f32x16_t acc[4][4];
+    f32x16_t acc[4][NJ];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
@@ -1024,15 +1050,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
     pp.load_w(2, 0);
     pp.lookup(qa, 1, 0);
     __syncthreads();
-    DxFrags f0;
-    dx_reads<true>(f0, lW, lD, 0, wa, wb, r, h);
+    DxFrags<NJ> f0;
+    dx_reads<true, NJ>(f0, lW, lD, 0, wa, wb, r, h);
     const int NT = pp.NT;
     int kt = 0;
     for (; kt + 1 < NT; kt += 2) {
-        dx_tile<0, F16>(pp, kt, acc, lW, lD, wa, wb, r, h, f0, qa);
-        dx_tile<1, F16>(pp, kt + 1, acc, lW, lD, wa, wb, r, h, f0, qa);
+        dx_tile<0, F16, TT>(pp, kt, acc, lW, lD, wa, wb, r, h, f0, qa);
+        dx_tile<1, F16, TT>(pp, kt + 1, acc, lW, lD, wa, wb, r, h, f0, qa);
     }
-    if (kt < NT) dx_tile<0, F16>(pp, kt, acc, lW, lD, wa, wb, r, h, f0, qa);
+    if (kt < NT) dx_tile<0, F16, TT>(pp, kt, acc, lW, lD, wa, wb, r, h, f0, qa);
 
     if (p.r > 0 && split == 0) {
         // LoRA term (s dY B^T) A^T: reduction over [hi | lo] of s dY B^T against A stacked twice
@@ -1050,9 +1076,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
             __syncthreads();
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                DxFrags f;
-                dx_reads<false>(f, lW, lD, s, wa, wb, r, h);
-                dx_mfma<F16>(acc, f);
+                DxFrags<NJ> f;
+                dx_reads<false, NJ>(f, lW, lD, s, wa, wb, r, h);
+                dx_mfma<F16, NJ>(acc, f);
             }
         }
     }
@@ -1072,7 +1098,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
 #pragma unroll
             for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -1097,18 +1123,45 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
         if constexpr (ADD) {
             // dx_add's tile goes to the same LDS tile first (whole rows); every
             // lane then adds the four values that its sums replace
-            otile_load(smem, p.dx_add, p.K, t0, k0, p.T, p.K);
+            otile_load<TT>(smem, p.dx_add, p.K, t0, k0, p.T, p.K);
             __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                    otile_put4<F16, ADD>(smem, acc[i][j], g, wb * 128 + j * 32 + r, wa * 128 + i * 32 + g * 8 + h * 4);
+                    otile_put4<F16, ADD>(smem, acc[i][j], g, (wb * NJ + j) * 32 + r, wa * 128 + i * 32 + g * 8 + h * 4);
         __syncthreads();
-        otile_store(smem, p.dx, p.K, t0, k0, p.T, p.K);
+        otile_store<TT>(smem, p.dx, p.K, t0, k0, p.T, p.K);
+    }
+}
+
+// TT2 > 0: a tile mix, as in k_fwd.
+template <bool F16, bool FUSED, bool SPLIT, bool ADD, int TT2>
+__global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, FusedGrads fz) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    build_pair_table16((lds8_t*)smem_raw + 4 * DxPipe<256>::kTile, cb);
+    const int ga = (int)ceil_div(p.K, 256), gb = (int)ceil_div(p.T, 256);
+    const int NT = (int)(p.N / 64);
+    int ta, tb;
+    if constexpr (SPLIT) {
+        const int split = (int)blockIdx.x / (ga * gb);
+        tile_of((int)blockIdx.x % (ga * gb), ga, gb, ta, tb);
+        dx_block<F16, true, ADD, 256>(p, smem_raw, ta, tb, split, split * NT / p.splits, (split + 1) * NT / p.splits);
+    } else if constexpr (TT2 == 0) {
+        tile_of((int)blockIdx.x, ga, gb, ta, tb);
+        dx_block<F16, false, ADD, 256>(p, smem_raw, ta, tb, 0, 0, NT);
+    } else {
+        const int n1 = p.na1 * gb;
+        if ((int)blockIdx.x < n1) {
+            tile_of((int)blockIdx.x, p.na1, gb, ta, tb);
+            dx_block<F16, false, ADD, 256>(p, smem_raw, ta, tb, 0, 0, NT);
+        } else {
+            tile_of((int)blockIdx.x - n1, ga - p.na1, (int)ceil_div(p.T, TT2), ta, tb);
+            dx_block<F16, false, ADD, TT2>(p, smem_raw, p.na1 + ta, tb, 0, 0, NT);
+        }
     }
 
     if constexpr (FUSED) {
@@ -1156,32 +1209,39 @@ hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, c
                       const LoraPlan& pl, const uint8_t* ws, uint16_t* y, hipStream_t s, bool f16,
                       const Epilogue* epi) {
     const bool split = pl.s_fwd > 1;
+    const TileMix mix = split ? TileMix{} : tile_mix(pl.N, pl.T);
     FwdArgs a{x, codes, sc.fp8, sc.sup, sc.absmax, lora_b, reinterpret_cast<const uint16_t*>(ws + pl.off_ps_hi),
               reinterpret_cast<const uint16_t*>(ws + pl.off_ps_lo), y,
               pl.T, pl.K, pl.N, pl.r, pl.r_pad,
-              split ? reinterpret_cast<float*>(const_cast<uint8_t*>(ws) + pl.off_fsp) : nullptr, pl.s_fwd};
-    const size_t lds = kFwdSmem;
-    const int64_t tiles = ceil_div(pl.N, 256) * ceil_div(pl.T, 256) * (split ? pl.s_fwd : 1);
+              split ? reinterpret_cast<float*>(const_cast<uint8_t*>(ws) + pl.off_fsp) : nullptr, pl.s_fwd, mix.na1};
+    const int64_t tiles = split ? ceil_div(pl.N, 256) * ceil_div(pl.T, 256) * pl.s_fwd : mix.blocks(pl.N, pl.T);
     const Epilogue ep = epi ? *epi : Epilogue{};
     auto go = [&](auto kern) {
-        hipError_t e = set_smem(kern, lds);
+        hipError_t e = set_smem(kern, kFwdSmem);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), lds, s, a, host_codebook(), ep);
+        hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), kFwdSmem, s, a, host_codebook(), ep);
         return hipGetLastError();
     };
+    // storage and type: fp16 has no single-quantization entry points
+    auto pick = [&](auto split_c, auto epi_c, auto tt2) {
+        constexpr bool S = decltype(split_c)::value, E = decltype(epi_c)::value;
+        constexpr int T2 = decltype(tt2)::value;
+        if (f16) return go(k_fwd<false, true, S, E, T2>);
+        return sc.single() ? go(k_fwd<true, false, S, E, T2>) : go(k_fwd<false, false, S, E, T2>);
+    };
     if (split) {
-        hipError_t e;
-        if (sc.single()) e = f16 ? go(k_fwd<true, true, true, false>) : go(k_fwd<true, false, true, false>);
-        else e = f16 ? go(k_fwd<false, true, true, false>) : go(k_fwd<false, false, true, false>);
+        hipError_t e = pick(std::true_type{}, std::false_type{}, std::integral_constant<int, 0>{});
         if (e != hipSuccess) return e;
         return split_sum(a.part, pl.s_fwd, pl.N, pl.T, y, s, f16, epi);
     }
-    if (epi) {
-        if (f16) return sc.single() ? go(k_fwd<true, true, false, true>) : go(k_fwd<false, true, false, true>);
-        return sc.single() ? go(k_fwd<true, false, false, true>) : go(k_fwd<false, false, false, true>);
-    }
-    if (f16) return sc.single() ? go(k_fwd<true, true, false, false>) : go(k_fwd<false, true, false, false>);
-    return sc.single() ? go(k_fwd<true, false, false, false>) : go(k_fwd<false, false, false, false>);
+    auto pick_mix = [&](auto epi_c) {
+        switch (mix.tt2) {
+            case 192: return pick(std::false_type{}, epi_c, std::integral_constant<int, 192>{});
+            case 128: return pick(std::false_type{}, epi_c, std::integral_constant<int, 128>{});
+            default: return pick(std::false_type{}, epi_c, std::integral_constant<int, 0>{});
+        }
+    };
+    return epi ? pick_mix(std::true_type{}) : pick_mix(std::false_type{});
 }
 
 ScalesJob scales_job_for(BlockScales sc, const LoraPlan& pl, uint8_t* ws) {
@@ -1200,35 +1260,42 @@ hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, c
         if (e0 != hipSuccess) return e0;
     }
     const bool split = pl.s_dx > 1;
+    // (the fused gradients' blocks are laid out for a grid of whole tiles)
+    const TileMix mix = split || fused ? TileMix{} : tile_mix(pl.K, pl.T);
     float* part = split ? reinterpret_cast<float*>(const_cast<uint8_t*>(ws) + (fused ? pl.off_dxp_fused : pl.off_dxp))
                         : nullptr;
     DxArgs a{dy, codes, sc.fp8, sc.sup, lora_a, reinterpret_cast<const uint16_t*>(ws + pl.off_gs_hi),
              reinterpret_cast<const uint16_t*>(ws + pl.off_gs_lo), sclt, dx, dx_add,
-             pl.T, pl.K, pl.N, pl.r, pl.r_pad, part, pl.s_dx};
-    const size_t lds = kDxSmem;
-    const int64_t tiles = ceil_div(pl.K, 256) * ceil_div(pl.T, 256) * (split ? pl.s_dx : 1);
+             pl.T, pl.K, pl.N, pl.r, pl.r_pad, part, pl.s_dx, mix.na1};
+    const int64_t tiles = split ? ceil_div(pl.K, 256) * ceil_div(pl.T, 256) * pl.s_dx : mix.blocks(pl.K, pl.T);
     FusedGrads f = fused ? *fused : FusedGrads{};
     f.waves = (int)tiles * 4;                         // the grid's waves share the gradient blocks
     auto go = [&](auto kern) {
-        hipError_t e = set_smem(kern, lds);
+        hipError_t e = set_smem(kern, kDxSmem);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), lds, s, a, host_codebook(), f);
+        hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(kThreads), kDxSmem, s, a, host_codebook(), f);
         return hipGetLastError();
     };
-    hipError_t e;
     if (split) {
-        if (fused) e = f16 ? go(k_dx<true, true, true, false>) : go(k_dx<false, true, true, false>);
-        else e = f16 ? go(k_dx<true, false, true, false>) : go(k_dx<false, false, true, false>);
+        hipError_t e;
+        if (fused) e = f16 ? go(k_dx<true, true, true, false, 0>) : go(k_dx<false, true, true, false, 0>);
+        else e = f16 ? go(k_dx<true, false, true, false, 0>) : go(k_dx<false, false, true, false, 0>);
         if (e != hipSuccess) return e;
         const Epilogue add{kActNone, nullptr, nullptr, dx_add, nullptr, nullptr, nullptr};
         return split_sum(part, pl.s_dx, pl.K, pl.T, dx, s, f16, dx_add ? &add : nullptr);
     }
-    if (dx_add) {
-        if (fused) return f16 ? go(k_dx<true, true, false, true>) : go(k_dx<false, true, false, true>);
-        return f16 ? go(k_dx<true, false, false, true>) : go(k_dx<false, false, false, true>);
+    if (fused) {                                      // never with dx_add
+        return f16 ? go(k_dx<true, true, false, false, 0>) : go(k_dx<false, true, false, false, 0>);
     }
-    if (fused) return f16 ? go(k_dx<true, true, false, false>) : go(k_dx<false, true, false, false>);
-    return f16 ? go(k_dx<true, false, false, false>) : go(k_dx<false, false, false, false>);
+    auto pick = [&](auto add_c) {
+        constexpr bool A = decltype(add_c)::value;
+        switch (mix.tt2) {
+            case 192: return f16 ? go(k_dx<true, false, false, A, 192>) : go(k_dx<false, false, false, A, 192>);
+            case 128: return f16 ? go(k_dx<true, false, false, A, 128>) : go(k_dx<false, false, false, A, 128>);
+            default: return f16 ? go(k_dx<true, false, false, A, 0>) : go(k_dx<false, false, false, A, 0>);
+        }
+    };
+    return dx_add ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace ql

@@ -68,6 +68,42 @@ inline int gemm_splits(int64_t T, int64_t L, int64_t C, size_t max_bytes) {
     return bs;
 }
 
+// Tile mix of an unsplit 256-column tile GEMM (out [T][C], one workgroup per
+// tile and CU): where the last round of 256-token tiles leaves CUs idle, its
+// part of the columns takes smaller tiles, as many as the round has room for.
+// Column tiles [0, na1) keep 256 tokens and fill the rounds before it (none with
+// na1 = 0), the others take tt2 tokens; tt2 = 0 is no mix.  Outputs keep their
+// bits (the same sum in the same order).  Without and with the mix, us:
+//   C = 11008, T = 2048 (one round, then 176 tiles of 128 for 88):   L = 4096
+//     forward 236 / 220, dX 244 / 221
+//   C = 11008, T = 4096 (two rounds, then 242 tiles of 192 for 176): L = 4096
+//     forward 352 / 348, dX 380 / 367;  C = 22016, T = 2048, L = 8192: 664 / 658
+// The gain is less than the idle CUs suggest because fewer busy CUs also run
+// faster; 224-token tiles (C = 11008, T = 1000) gained nothing.
+struct TileMix {
+    int na1 = 0, tt2 = 0;
+    int64_t blocks(int64_t C, int64_t T) const {
+        const int64_t ga = ceil_div(C, 256), gb = ceil_div(T, 256);
+        return tt2 ? na1 * gb + (ga - na1) * ceil_div(T, tt2) : ga * gb;
+    }
+};
+inline TileMix tile_mix(int64_t C, int64_t T) {
+    const int64_t ga = ceil_div(C, 256), gb = ceil_div(T, 256), tiles = ga * gb;
+    const int64_t full = tiles / 256;                 // whole rounds of 256-token tiles
+    TileMix m;
+    if (tiles % 256 == 0 || full > 8) return m;       // nothing to gain, or too little of the whole
+    const int64_t na1 = full * 256 / gb;              // column tiles of those rounds
+    const int64_t room = (full + 1) * 256 - na1 * gb;
+    for (int tt : {128, 192}) {
+        if ((ga - na1) * ceil_div(T, tt) <= room) {
+            m.na1 = (int)na1;
+            m.tt2 = tt;
+            return m;
+        }
+    }
+    return m;
+}
+
 constexpr size_t kSplitPartialMax = size_t(64) << 20;
 
 struct LoraPlan {

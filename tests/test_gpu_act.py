@@ -376,3 +376,26 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(ref, outs):
             assert torch.equal(a, b), k
+
+
+@pytest.mark.parametrize("T,N,K", [(2048, 22016, 64), (2000, 21952, 128), (2048, 11008, 64), (1000, 11008, 64),
+                                   (700, 16384, 64), (130, 320, 128)])
+def test_tile_mixes(T, N, K):
+    """Grids whose last round takes smaller token tiles: two full rounds then 192 (22016 columns at
+    2048 tokens, and ragged in both directions), one then 128, a round without a mix, and single
+    rounds of 192 and 128 tokens.  Forward with an epilogue and without, and dX of the transposed shape with and
+    without a gradient to add."""
+    say(f"[tile mix] T={T} N={N} K={K}")
+    c = Case(T, N, K, 8)
+    y = api.qlora_linear_act_fwd(c.x, c.qw, c.a, c.b, c.s, bias=c.bias, act="silu", mul=c.mul, residual=c.res)
+    p = api.qlora_linear_fwd(c.x, c.qw, c.a, c.b, c.s)
+    torch.cuda.synchronize()
+    check(y, oracle.act_fwd(f64(c.x), c.wd, *c.ab64(), c.s, f64(c.bias), "silu", f64(c.mul), f64(c.res))[0], "Y")
+    check(p, oracle.act_fwd(f64(c.x), c.wd, *c.ab64(), c.s)[0], "plain Y")
+    d = Case(T, K, N, 8)                                     # K outputs, N inputs: dX is [T, N]
+    g = api.qlora_linear_act_bwd(d.dy, d.qw, d.a, d.b, d.s, dx_add=d.add)
+    dx = api.qlora_linear_bwd_input(d.dy, d.qw, d.a, d.b, d.s)[0]
+    torch.cuda.synchronize()
+    ref = oracle.act_bwd(f64(d.dy), d.wd, *d.ab64(), d.s)
+    check(dx, ref["dx"], "plain dX")
+    check(g.dx, ref["dx"] + f64(d.add), "dX")
