@@ -147,7 +147,7 @@ int nf4_dequantize_dq_grouped(int count, const nf4_tensor* tensors, void* stream
  *   Returns 0 for sizes the entry points would reject.  The size is not
  *   monotone in T: 16 < T <= 96 keeps one set of split partials per 16-token
  *   window and can need more than a larger T (for example about 34 MB at
- *   T = 96 against about 26 MB at T = 4096 on an 11008 x 4096 weight with
+ *   T = 96 against about 25 MB at T = 4096 on an 11008 x 4096 weight with
  *   r = 64), and a mid-size T whose 256 x 256 output tiles are too few to
  *   fill the chip splits the reduction over several workgroups with fp32
  *   partial tiles (at most 64 MiB; 64 MiB for a 4096 x 4096 weight at

@@ -353,7 +353,7 @@ struct ActBwdPlan {
     size_t off_dz, off_gpart, off_ppart, off_part, bytes;
     int s_g, s_p;
     static int splits(int64_t T, int64_t L, int64_t r) {
-        const int64_t s = std::min<int64_t>(16, std::min<int64_t>(512 / ql::ceil_div(T, 64), L / 64));
+        const int64_t s = std::min<int64_t>(16, std::min<int64_t>(256 / ql::ceil_div(T, 64), L / 64));
         return r > 0 ? (int)std::max<int64_t>(1, s) : 0;
     }
     ActBwdPlan(int64_t T, int64_t K, int64_t N, int64_t r)

@@ -590,8 +590,8 @@ QL_DEV void fwd_block(const FwdArgs& p, const Epilogue& ep, uint8_t* smem_raw, i
                         lt[loff(32 * w + 8 * g + 4 * h + v, 32 * j + r)] = acc[i][j][4 * g + v];
             __syncthreads();
 #pragma unroll 4
-            for (int e = threadIdx.x; e < 128 * 64; e += kThreads) {     // 64 float4 per row
-                const int row = e >> 6, c4 = e & 63;
+            for (int e = threadIdx.x; e < 128 * (TT / 4); e += kThreads) {   // TT / 4 float4 per row
+                const int row = e / (TT / 4), c4 = e % (TT / 4);
                 const int64_t n = n0 + 64 * (row >> 5) + 32 * i + (row & 31);
                 const int64_t t = t0 + 4 * c4;
                 if (n < p.N && t < p.T) {                                 // t + 3 < ldp
@@ -673,7 +673,8 @@ QL_DEV void fwd_block(const FwdArgs& p, const Epilogue& ep, uint8_t* smem_raw, i
 // TT2 > 0: the grid is a tile mix.  Workgroups [0, n1) take the 256-token tiles
 // of the first na1 row tiles of W, the rest TT2-token tiles of the others (all of
 // them with na1 = 0).  Every output is the same sum in the same order whatever
-// its tile's size, so the bits do not depend on the mix.
+// its tile's size, so the bits do not depend on the mix.  With SPLIT every tile
+// has TT2 tokens (256 for TT2 = 0).
 template <bool SQ, bool F16, bool SPLIT, bool EPI, int TT2>
 __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epilogue ep) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -682,10 +683,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_fwd(FwdArgs p, Codebook cb, Epi
     const int KT = (int)(p.K / 64);
     int ta, tb;
     if constexpr (SPLIT) {
-        const int split = (int)blockIdx.x / (ga * gb);
-        tile_of((int)blockIdx.x % (ga * gb), ga, gb, ta, tb);
-        fwd_block<SQ, F16, true, EPI, 256>(p, ep, smem_raw, ta, tb, split, split * KT / p.splits,
-                                           (split + 1) * KT / p.splits);
+        constexpr int TT = TT2 ? TT2 : 256;
+        const int gt = (int)ceil_div(p.T, TT), split = (int)blockIdx.x / (ga * gt);
+        tile_of((int)blockIdx.x % (ga * gt), ga, gt, ta, tb);
+        fwd_block<SQ, F16, true, EPI, TT>(p, ep, smem_raw, ta, tb, split, split * KT / p.splits,
+                                          (split + 1) * KT / p.splits);
     } else if constexpr (TT2 == 0) {
         tile_of((int)blockIdx.x, ga, gb, ta, tb);
         fwd_block<SQ, F16, false, EPI, 256>(p, ep, smem_raw, ta, tb, 0, 0, KT);
@@ -1103,12 +1105,12 @@ QL_DEV void dx_block(const DxArgs& p, uint8_t* smem_raw, int ta, int tb, int spl
                     for (int g = 0; g < 4; ++g)
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            lt[loff(64 * wa + 32 * ii + 8 * g + 4 * h + v, wb * 128 + 32 * j + r)] =
+                            lt[loff(64 * wa + 32 * ii + 8 * g + 4 * h + v, (wb * NJ + j) * 32 + r)] =
                                 acc[2 * hf + ii][j][4 * g + v];
             __syncthreads();
 #pragma unroll 4
-            for (int e = threadIdx.x; e < 128 * 64; e += kThreads) {     // 64 float4 per row
-                const int row = e >> 6, c4 = e & 63;
+            for (int e = threadIdx.x; e < 128 * (TT / 4); e += kThreads) {   // TT / 4 float4 per row
+                const int row = e / (TT / 4), c4 = e % (TT / 4);
                 const int64_t k = k0 + 128 * (row >> 6) + 64 * hf + (row & 63);
                 const int64_t t = t0 + 4 * c4;
                 if (k < p.K && t < p.T) {                                 // t + 3 < ldp
@@ -1138,7 +1140,7 @@ QL_DEV void dx_block(const DxArgs& p, uint8_t* smem_raw, int ta, int tb, int spl
     }
 }
 
-// TT2 > 0: a tile mix, as in k_fwd.
+// TT2: a tile mix, or the split tiles' tokens, as in k_fwd.
 template <bool F16, bool FUSED, bool SPLIT, bool ADD, int TT2>
 __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, FusedGrads fz) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -1147,9 +1149,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_dx(DxArgs p, Codebook cb, Fused
     const int NT = (int)(p.N / 64);
     int ta, tb;
     if constexpr (SPLIT) {
-        const int split = (int)blockIdx.x / (ga * gb);
-        tile_of((int)blockIdx.x % (ga * gb), ga, gb, ta, tb);
-        dx_block<F16, true, ADD, 256>(p, smem_raw, ta, tb, split, split * NT / p.splits, (split + 1) * NT / p.splits);
+        constexpr int TT = TT2 ? TT2 : 256;
+        const int gt = (int)ceil_div(p.T, TT), split = (int)blockIdx.x / (ga * gt);
+        tile_of((int)blockIdx.x % (ga * gt), ga, gt, ta, tb);
+        dx_block<F16, true, ADD, TT>(p, smem_raw, ta, tb, split, split * NT / p.splits, (split + 1) * NT / p.splits);
     } else if constexpr (TT2 == 0) {
         tile_of((int)blockIdx.x, ga, gb, ta, tb);
         dx_block<F16, false, ADD, 256>(p, smem_raw, ta, tb, 0, 0, NT);
@@ -1230,7 +1233,12 @@ hipError_t launch_fwd(const uint16_t* x, const uint8_t* codes, BlockScales sc, c
         return sc.single() ? go(k_fwd<true, false, S, E, T2>) : go(k_fwd<false, false, S, E, T2>);
     };
     if (split) {
-        hipError_t e = pick(std::true_type{}, std::false_type{}, std::integral_constant<int, 0>{});
+        hipError_t e;
+        switch (split_tokens(pl.T)) {
+            case 128: e = pick(std::true_type{}, std::false_type{}, std::integral_constant<int, 128>{}); break;
+            case 192: e = pick(std::true_type{}, std::false_type{}, std::integral_constant<int, 192>{}); break;
+            default: e = pick(std::true_type{}, std::false_type{}, std::integral_constant<int, 0>{}); break;
+        }
         if (e != hipSuccess) return e;
         return split_sum(a.part, pl.s_fwd, pl.N, pl.T, y, s, f16, epi);
     }
@@ -1278,7 +1286,10 @@ hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, BlockScales sc, c
     };
     if (split) {
         hipError_t e;
+        const int tt = split_tokens(pl.T);
         if (fused) e = f16 ? go(k_dx<true, true, true, false, 0>) : go(k_dx<false, true, true, false, 0>);
+        else if (tt == 128) e = f16 ? go(k_dx<true, false, true, false, 128>) : go(k_dx<false, false, true, false, 128>);
+        else if (tt == 192) e = f16 ? go(k_dx<true, false, true, false, 192>) : go(k_dx<false, false, true, false, 192>);
         else e = f16 ? go(k_dx<true, false, true, false, 0>) : go(k_dx<false, false, true, false, 0>);
         if (e != hipSuccess) return e;
         const Epilogue add{kActNone, nullptr, nullptr, dx_add, nullptr, nullptr, nullptr};
