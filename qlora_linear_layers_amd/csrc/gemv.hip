@@ -491,7 +491,8 @@ constexpr bool fin_wide(int64_t T, int64_t columns) { return T <= 8 && columns >
 constexpr int fin_cols(bool wide) { return wide ? 128 : 64; }
 //
 // EPI: Y leaves through the epilogue of its problem, whose operands (bias, mul,
-// residual) are loaded with the partials; a 64-column block of a checkpoint of
+// residual) are loaded with the partials (no time beyond the plain form's: 4.2 to
+// 5.4 us at T = 1 on 4096 -> 11008, the launch pair 15.5); a 64-column block of a checkpoint of
 // Z is 32 lanes (CPL = 2) or the whole wave.
 struct EpiGroup {
     Epilogue e[kMaxGroup];

@@ -56,7 +56,8 @@ constexpr size_t kGradSmem = (size_t)4 * 8 * 4 * 64 * 4 * 4;   // the wave sums,
 // column cb 128 + 8 (l % 16) + i; acc[i][jt][v] is column
 // cb 128 + 8 (4 (l / 16) + v) + i, rank j0 + 16 jt + l % 16).  The chunks are
 // walked from chunk `rot` on, in a fixed order.  Q8: S is an 8-bit checkpoint;
-// a lane loads the eight codes and the scale of each of its eight tokens.
+// a lane loads the eight codes and the scale of each of its eight tokens (the
+// dA of 2048 x 4096 with the dB of 2048 x 11008: 24 us with X in 8 bits or 16).
 template <bool F16, bool Q8 = false>
 QL_DEV void grad_accumulate(const GradArgs& a, int cb, int64_t tw, int nch, int rot, int64_t j0,
                             f32x4_t (&acc)[8][4]) {
