@@ -80,6 +80,7 @@ constexpr int kDecThreads = 64 * kKW * kRG;
 constexpr int kDecRows = 64 * kRG;  // W rows per workgroup
 constexpr int kDecK = 128 * kKW;    // k per workgroup
 static_assert(kRG * kKW * 4 * 64 * 16 <= (int)kNarrowTableBytes, "wave sums must fit over the pair table");
+static_assert(kKW == 4 && kRG == 2, "k_gemv_win: four tiles for four waves, two halves of the table's space");
 static_assert(4 * 2 * kGemvMaxT * 64 * 4 <= (int)kNarrowTableBytes, "LoRA block sums must fit in the table's space");
 static_assert(kRG * kKW * 4 * 8 * 64 * 4 <= (int)kWideTableBytes, "VALU wave sums (8 tokens) must fit too");
 constexpr int kLoraSlice = 256;   // k per LoRA down-projection workgroup (one 64-k chunk per wave)
@@ -93,7 +94,7 @@ constexpr size_t kDecLds = kWideTableBytes;   // VALU form: pair table; later re
 // reads X as LDS broadcasts; the eight (wave, half) sums of every output are
 // then added in LDS in that order.  Every thread of the workgroup reaches
 // every barrier.
-template <int TT, bool F16>
+template <int TT, bool F16, int NT>                                   // NT: threads of the workgroup
 __device__ __forceinline__ void lora_down_block(const GemvArgs& p, uint8_t* dyn, int lb) {
     typedef __attribute__((address_space(3))) float g_lds_f32_t;
     lds8_t* xl = (lds8_t*)dyn;                                         // [TT][kLoraSlice] bf16
@@ -104,7 +105,7 @@ __device__ __forceinline__ void lora_down_block(const GemvArgs& p, uint8_t* dyn,
     const int64_t j0 = (int64_t)jc * 64 + 2 * q;                       // this lane's two ranks
     const int64_t k0 = (int64_t)kl * kLoraSlice;
     const rsrc_t rx = make_rsrc(p.x, p.T * p.K * 2);
-    for (int ch = threadIdx.x; ch < TT * (kLoraSlice / 8); ch += kDecThreads) {
+    for (int ch = threadIdx.x; ch < TT * (kLoraSlice / 8); ch += NT) {
         const int t = ch / (kLoraSlice / 8);
         const int64_t kk = k0 + (ch % (kLoraSlice / 8)) * 8;
         const u32x4_t v = bload16(rx, (t < p.T && kk < p.K) ? (uint32_t)((t * p.K + kk) * 2) : kOOB, 0);
@@ -158,7 +159,7 @@ __device__ __forceinline__ void lora_down_block(const GemvArgs& p, uint8_t* dyn,
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < TT * 64; i += kDecThreads) {
+    for (int i = threadIdx.x; i < TT * 64; i += NT) {
         const int t = i >> 6, jj = i & 63;
         if (t < p.T) {
             float v = red[t * 64 + jj];
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
     if (bid < lora_total) {
         const int i = group_find(grp.lora_end, grp.count, bid);
         const GemvArgs p = grp.p[i];
-        lora_down_block<TT, F16>(p, dyn, bid - (i ? grp.lora_end[i - 1] : 0));
+        lora_down_block<TT, F16, kDecThreads>(p, dyn, bid - (i ? grp.lora_end[i - 1] : 0));
         return;
     }
     const int gi = group_find(grp.base_end, grp.count, bid);
@@ -370,30 +371,32 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
 // lane, against four), so the weight stream and the dequantization do not grow
 // with T.  4096 x 4096 at 61 tokens (no adapter): 20.7 us as four windows of
 // k_gemv, whose VALU work is four dequantizations of the weight.  Sums and
-// their order are those of k_gemv, so are the partials.  The k waves of a row
-// group are added one window at a time, alternating two 32 KB LDS buffers (one
-// over the table), one barrier per window.
+// their order are those of k_gemv, so are the partials.  A workgroup takes one
+// group of 64 rows, so that more of them share a CU (the registers allow three
+// waves a SIMD at G = 4) and wait for memory at different times.  The k waves are
+// added one window at a time, alternating two 16 KB halves of the table's LDS,
+// one barrier per window.
+constexpr int kWinThreads = 64 * kKW;   // one group of 64 W rows per workgroup
 template <int G, bool SQ, bool F16>
-__global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Codebook cb) {
+__global__ __launch_bounds__(kWinThreads, G <= 2 ? 4 : 2) void k_gemv_win(GemvGroup grp, Codebook cb) {
     extern __shared__ __align__(16) uint8_t dyn[];
     const int bid = (int)blockIdx.x;
     const int lora_total = grp.lora_end[grp.count - 1];
     if (bid < lora_total) {
         const int i = group_find(grp.lora_end, grp.count, bid);
         const GemvArgs p = grp.p[i];
-        lora_down_block<kGemvMaxT, F16>(p, dyn, bid - (i ? grp.lora_end[i - 1] : 0));
+        lora_down_block<kGemvMaxT, F16, kWinThreads>(p, dyn, bid - (i ? grp.lora_end[i - 1] : 0));
         return;
     }
     const GemvArgs p = grp.p[0];                                       // the weight of every window
     const int bx = bid - lora_total;
     lds8_t* tbl = (lds8_t*)dyn;
     const int lane = threadIdx.x & 63;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wave = wv % kKW, rg = wv / kKW;                          // k step, row group
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // k step
     const int nl = lane & 15, g = lane >> 4;
-    const int nb = (int)ceil_div(p.N, kDecRows);
+    const int nb = (int)(p.N / 64);
     const int rb = bx % nb, ks = bx / nb;
-    const int64_t n0 = (int64_t)rb * kDecRows + 64 * rg;
+    const int64_t n0 = (int64_t)rb * 64;                               // N % 64 == 0: all 64 rows exist
     const int64_t kk = (int64_t)ks * kDecK + 128 * wave + 32 * g;      // this lane's 32 k
     const bool kok = kk < p.K;
     const rsrc_t rc = make_rsrc(p.codes, p.N * p.K / 2);
@@ -405,7 +408,7 @@ __global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Code
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int64_t n = n0 + 16 * c + nl;
-        const bool ok = kok && n < p.N;
+        const bool ok = kok;
         const int64_t blk = n * (p.K / 64) + kk / 64;
         cw[c] = bload16(rc, ok ? (uint32_t)(n * (p.K / 2) + kk / 2) : kOOB, 0);
         if constexpr (SQ) {
@@ -424,7 +427,7 @@ __global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Code
 #pragma unroll
         for (int j = 0; j < 4; ++j) xv[q][j] = bload16(rx, xo, (uint32_t)(16 * j));
     }
-    if (threadIdx.x < 256) build_pair_table16(tbl, cb);
+    build_pair_table16(tbl, cb);
     __syncthreads();
 
     const uint32_t lane8 = lds_addr(tbl) + (uint32_t)(lane & 15) * 8u;
@@ -451,20 +454,19 @@ __global__ __launch_bounds__(kDecThreads, 2) void k_gemv_win(GemvGroup grp, Code
     __syncthreads();                                                   // the table is no longer read
 #pragma unroll
     for (int q = 0; q < G; ++q) {
-        f32x4_t* red = reinterpret_cast<f32x4_t*>(dyn + (q & 1) * kNarrowTableBytes) + rg * (kKW * 4 * 64);
+        f32x4_t* red = reinterpret_cast<f32x4_t*>(dyn) + (q & 1) * (kKW * 4 * 64);
 #pragma unroll
         for (int c = 0; c < 4; ++c) red[(wave * 4 + c) * 64 + lane] = acc[q][c];
         __syncthreads();                       // also: buffer q & 1 was read before the barrier of window q - 1
-        if (wave < 4) {
-            const int c = wave, l = lane;
+        {
+            const int c = wave, l = lane;                              // kKW waves, four 16-row tiles
             f32x4_t v = red[c * 64 + l];
 #pragma unroll
             for (int w = 1; w < kKW; ++w) v += red[(w * 4 + c) * 64 + l];
             const int64_t n = n0 + 16 * c + (l & 15);
             float* part = grp.p[q].part + (int64_t)ks * kGemvMaxT * p.N;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n < p.N) part[(int64_t)(4 * (l >> 4) + e) * p.N + n] = v[e];
+            for (int e = 0; e < 4; ++e) part[(int64_t)(4 * (l >> 4) + e) * p.N + n] = v[e];
         }
     }
 }
@@ -775,15 +777,16 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     const bool sq = probs[0].sc.single();
     if (dot && (sq || f16)) return hipErrorInvalidValue;             // the VALU form serves the bf16 DQ path
     const Codebook& cb = host_codebook();
-    const dim3 grid((unsigned)(nl + (windows ? g.p[0].gemv_blocks : nbase)));
+    const dim3 grid((unsigned)(nl + (windows ? (int)(probs[0].N / 64) * g.p[0].KS : nbase)));
     hipError_t ae = hipSuccess;
     size_t lds = dot ? kDecLds : (size_t)kNarrowTableBytes;
+    const dim3 threads(windows ? kWinThreads : kDecThreads);
     auto go = [&](auto kern) {
         // more than 64 KB of dynamic LDS: above the default limit
         if (lds > 65536)
             ae = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)lds);
-        if (ae == hipSuccess) hipLaunchKernelGGL(kern, grid, dim3(kDecThreads), lds, s, g, cb);
+        if (ae == hipSuccess) hipLaunchKernelGGL(kern, grid, threads, lds, s, g, cb);
     };
     auto pick = [&](auto tt) {
         constexpr int TT = decltype(tt)::value;
@@ -799,7 +802,6 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     };
     auto pick_win = [&](auto gg) {
         constexpr int G = decltype(gg)::value;
-        lds = 2 * (size_t)kNarrowTableBytes;
         if (sq) f16 ? go(k_gemv_win<G, true, true>) : go(k_gemv_win<G, true, false>);
         else f16 ? go(k_gemv_win<G, false, true>) : go(k_gemv_win<G, false, false>);
     };
