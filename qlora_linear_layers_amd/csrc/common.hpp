@@ -357,10 +357,9 @@ hipError_t launch_dequantize(const uint8_t* codes, BlockScales sc, int64_t numel
 // Forward calls with at most this many tokens take the decode (small-M MFMA) path.
 constexpr int64_t kGemvMaxT = 16;
 // Forward sizes T (kGemvMaxT < T <= kChunkMaxT) that run as kGemvMaxT-token
-// windows through one grouped decode launch: each window streams the weight.
-// Up to 96 tokens that beats the split-k MFMA tiles (the LLaMA-7B projections:
-// 371 against 397 us at T = 96); from about 100 tokens the tiles win (395
-// against 456 us at T = 128).
+// windows of one decode launch pair, which reads and dequantizes the weight once.
+// The seven LLaMA-7B projections (r = 64): 158 us at T = 32, 216 at 64 and 287 at
+// 96, about 36 us a window; the MFMA tiles take 323 us at T = 97 and 313 at 128.
 constexpr int64_t kChunkMaxT = 96;
 struct LoraPlan;
 struct Epilogue;              // output epilogue of the forward (act.hpp); one per problem of a group, or none

@@ -370,7 +370,8 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
 // each weight fragment meets G token fragments (4 G MFMAs per 64 rows x 32 k and
 // lane, against four), so the weight stream and the dequantization do not grow
 // with T.  4096 x 4096 at 61 tokens (no adapter): 20.7 us as four windows of
-// k_gemv, whose VALU work is four dequantizations of the weight.  Sums and
+// k_gemv, whose VALU work is four dequantizations of the weight, 11.6 here; with
+// a rank-64 adapter at T = 64 14.6 us, 27 us on 11008 x 4096.  Sums and
 // their order are those of k_gemv, so are the partials.  A workgroup takes one
 // group of 64 rows, so that more of them share a CU (the registers allow three
 // waves a SIMD at G = 4) and wait for memory at different times.  The k waves are
@@ -484,12 +485,19 @@ __global__ __launch_bounds__(kWinThreads, G <= 2 ? 4 : 2) void k_gemv_win(GemvGr
 // in registers.  No LDS and no barrier: the B column, the base partials and
 // the first slice partials are all issued before the first sum, so for the
 // decode shapes the kernel waits for one round of loads.
-// CPL columns per lane: 2 up to T = 8, 1 above (more workgroups for the
-// 8-wave, 16-token case), and 1 with one token per wave where the launch has at
-// most 8192 columns, whose 128-column workgroups would be 64 at most (T = 7 on
-// 11008 -> 4096: 21.2 us the launch pair with two columns, 19.8 with one; T = 8
-// on 4096 -> 11008 the same either way, on 8192 -> 22016 44.1 against 46.9).
-constexpr bool fin_wide(int64_t T, int64_t columns) { return T <= 8 && columns > 8192; }
+// CPL columns per lane: 2 up to T = 8, 1 for a 16-token call (more workgroups for
+// its eight waves: 6.4 against 7.2 us), and 1 with one token per wave where the
+// launch has at most 8192 columns (over all its problems), whose 128-column
+// workgroups would be 64 at most (T = 7 on 11008 -> 4096: 21.2 us the launch pair
+// with two columns, 19.8 with one; T = 8 on 4096 -> 11008 the same either way, on
+// 8192 -> 22016 44.1 against 46.9).  The windows of a small prefill take 2 where
+// 64-column workgroups would be more than one a CU, since each wave reads its lanes'
+// B columns (T = 32 on 4096 -> 11008 10.9 -> 7.5 us, 64 17.3 -> 14.2, 96 25.6 -> 19.9,
+// 96 on 11008 -> 4096 16.3 -> 11.7; with one a CU, 64 on 11008 -> 4096, 9.6 with one
+// column and 10.7 with two).
+constexpr bool fin_wide(int64_t T, int64_t columns, bool windows) {
+    return windows ? columns > 256 * 64 : T <= 8 && columns > 8192;
+}
 constexpr int fin_cols(bool wide) { return wide ? 128 : 64; }
 //
 // EPI: Y leaves through the epilogue of its problem, whose operands (bias, mul,
@@ -756,7 +764,7 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     int nl = 0, nbase = 0, nfin = 0;
     int64_t columns = 0;
     for (int i = 0; i < count; ++i) columns += probs[i].N;
-    const bool wide = fin_wide(T, columns);
+    const bool wide = fin_wide(T, columns, windows);
     for (int i = 0; i < count; ++i) {
         const GemvProblem& q = probs[i];
         GemvArgs& a = g.p[i];
