@@ -370,7 +370,7 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
 // each weight fragment meets G token fragments (4 G MFMAs per 64 rows x 32 k and
 // lane, against four), so the weight stream and the dequantization do not grow
 // with T.  4096 x 4096 at 61 tokens (no adapter): 20.7 us as four windows of
-// k_gemv, whose VALU work is four dequantizations of the weight, 11.6 here; with
+// k_gemv, whose VALU work is four dequantizations of the weight, 13 here; with
 // a rank-64 adapter at T = 64 14.6 us, 27 us on 11008 x 4096.  Sums and
 // their order are those of k_gemv, so are the partials.  A workgroup takes one
 // group of 64 rows, so that more of them share a CU (the registers allow three
