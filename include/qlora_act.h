@@ -19,7 +19,8 @@ extern "C" {
 #endif
 
 /* Activations.  gelu is z Phi(z) with the normal distribution function,
- * gelu_tanh its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+ * gelu_tanh its tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).
+ * relu's slope at 0 is 0; a NaN gives NaN in every activation and slope. */
 #define QLORA_ACT_NONE 0
 #define QLORA_ACT_RELU 1
 #define QLORA_ACT_SILU 2

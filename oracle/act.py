@@ -30,12 +30,12 @@ def act(z, name):
 
 
 def act_slope(z, name):
-    """act'(z) in fp64 (relu'(0) = 0)."""
+    """act'(z) in fp64 (relu'(0) = 0; NaN at NaN)."""
     z = np.asarray(z, dtype=np.float64)
     if name == "none":
         return np.ones_like(z)
     if name == "relu":
-        return (z > 0).astype(np.float64)
+        return np.where(np.isnan(z), z, (z > 0).astype(np.float64))
     if name == "silu":
         p = expit(z)
         return p + z * p * expit(-z)

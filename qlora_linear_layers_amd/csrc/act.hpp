@@ -49,32 +49,34 @@ QL_DEV float normal_cdf(float z, float& e) {
 
 template <int ACT>
 QL_DEV float act_value(float z) {
-    if constexpr (ACT == kActRelu) return z > 0.0f ? z : 0.0f;
+    if constexpr (ACT == kActRelu) return z <= 0.0f ? 0.0f : z;
     else if constexpr (ACT == kActSilu) return z * logistic(z);
     else if constexpr (ACT == kActGelu) { float e; return z * normal_cdf(z, e); }
     else if constexpr (ACT == kActGeluTanh) return z * logistic(2.0f * kTanhC * z * fmaf(kTanhA * z, z, 1.0f));
     else return z;
 }
 
-// act(z) and act'(z).  relu'(0) = 0.  The tanh form's slope is constant beyond
-// |z| = 32 (0 or 1 in fp32), and z is held inside that range there so that its
-// z^3 does not overflow into inf * 0.
+// act(z) and act'(z).  relu'(0) = 0.  A NaN comes out of both, relu's too, so that
+// it is not lost on the way to the gradients.  The silu slope adds v (1 - p) to p,
+// in that order: p + v first would lose p to v's rounding where z is large.  The
+// tanh form's slope is constant beyond |z| = 32 (0 or 1 in fp32), and z is held
+// inside that range there so that its z^3 does not overflow into inf * 0.
 template <int ACT>
 QL_DEV void act_slope(float z, float& v, float& d) {
     if constexpr (ACT == kActRelu) {
-        v = z > 0.0f ? z : 0.0f;
-        d = z > 0.0f ? 1.0f : 0.0f;
+        v = z <= 0.0f ? 0.0f : z;
+        d = z <= 0.0f ? 0.0f : z > 0.0f ? 1.0f : z;
     } else if constexpr (ACT == kActSilu) {
         const float p = logistic(z);
         v = z * p;
-        d = fmaf(-v, p, v + p);                              // p + v (1 - p)
+        d = fmaf(v, 1.0f - p, p);
     } else if constexpr (ACT == kActGelu) {
         float e;
         const float p = normal_cdf(z, e);
         v = z * p;
         d = fmaf(z * kInvSqrt2Pi, e, p);
     } else if constexpr (ACT == kActGeluTanh) {
-        const float c = __builtin_amdgcn_fmed3f(z, -32.0f, 32.0f);
+        const float c = z > 32.0f ? 32.0f : z < -32.0f ? -32.0f : z;
         const float p = logistic(2.0f * kTanhC * c * fmaf(kTanhA * c, c, 1.0f));
         v = z * p;
         d = fmaf(c * p * (1.0f - p), 2.0f * kTanhC * fmaf(3.0f * kTanhA * c, c, 1.0f), p);

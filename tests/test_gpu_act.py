@@ -142,6 +142,48 @@ def test_large_and_extreme_preactivations():
         assert torch.isfinite(g.dx).all() and torch.isfinite(g.d_bias).all(), act
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", [a for a in oracle.ACTS if a != "none"])
+def test_slopes_over_the_range(act, dtype):
+    """With one token d_bias is dY act'(Z) and d_mul dY act(Z), each rounded once.  Z covers the
+    type's magnitudes in both signs; the fp32 terms of a slope (p, and z times an exponentially
+    small factor) are good to a few 2^-24 of 1, or of the result where that is larger."""
+    dt, N = DT[dtype], 1024
+    top = 4.5 if dtype == "fp16" else 30.0
+    m = torch.logspace(-6, top, N // 2 - 32, dtype=torch.float64)
+    z = torch.cat([m, -m, torch.linspace(-12, 12, 63, dtype=torch.float64), torch.zeros(1, dtype=torch.float64)])
+    z = z.to(dt).reshape(1, N).cuda()
+    qw = api.nf4_quantize_dq(torch.ones(N, 64, dtype=dt, device="cuda"))
+    one = torch.ones(1, N, dtype=dt, device="cuda")
+    say(f"[act] slopes {act} {dtype}")
+    g = api.qlora_linear_act_bwd(one, qw, act=act, z=z, mul=one, bias_grad=True)
+    with np.errstate(all="ignore"):
+        rd, rv = oracle.act_slope(f64(z), act)[0], oracle.act(f64(z), act)
+    rd = np.where(np.isnan(rd), (f64(z)[0] > 0).astype(float), rd)      # 0 * inf in the fp64 tails of the tanh form
+    u = U[dt]
+    assert np.all(np.abs(f64(g.d_bias) - rd) <= u * np.abs(rd) + 2.0 ** -20)
+    assert np.all(np.abs(f64(g.d_mul) - rv) <= u * np.abs(rv) + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("act", oracle.ACTS)
+def test_nan_is_not_lost(act):
+    """A NaN pre-activation is NaN in Y, Z and its checkpoint, and in the gradients that read it."""
+    c = Case(3, 128, 64, 0)
+    x = c.x.clone()
+    x[1, 5] = float("nan")
+    say(f"[act] nan {act}")
+    y, z8 = api.qlora_linear_act_fwd(x, c.qw, act=act, mul=c.mul, save="z8")
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
+    z = api.act8_dequantize(z8)
+    assert torch.isnan(z[1]).all() and torch.isfinite(z[[0, 2]]).all()
+    for saved in (z, z8):
+        g = api.qlora_linear_act_bwd(c.dy, c.qw, act=act, z=saved, mul=c.mul)
+        assert torch.isnan(g.d_mul[1]).all() and torch.isfinite(g.d_mul[[0, 2]]).all()
+        assert torch.isfinite(g.dx[[0, 2]]).all()
+        if act != "none":
+            assert torch.isnan(g.dx[1]).all()
+
+
 # ------------------------------------------------------------------ checkpoints
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
