@@ -205,6 +205,23 @@ def _check_storage(qw):
         _count(qw.superscale, -(-n // 16384), "superscale")
 
 
+def _dev_storage(qw):
+    """The storage of a quantized weight as the kernels read and write it: dense GPU tensors of
+    their types (a host address, a narrower type or a strided view of the right count would be
+    read past its end)."""
+    _dev(qw.codes, torch.uint8, "codes")
+    if isinstance(qw, NF4WeightSQ):
+        _dev(qw.absmax, torch.float32, "absmax")
+    else:
+        _dev(qw.absmax_fp8, torch.uint8, "absmax_fp8")
+        _dev(qw.superscale, torch.float32, "superscale")
+
+
+def _dev_workspace(t):
+    """A caller's workspace: dense GPU memory of any type, of at least numel() bytes."""
+    _dev(t, None if t is None else t.dtype, "workspace")
+
+
 def _check_adapters(lora_a, lora_b, K, N):
     """Rank of the adapter pair A [K, r], B [r, N] (0 without an adapter)."""
     if (lora_a is None) != (lora_b is None):
@@ -279,6 +296,7 @@ def nf4_quantize_dq_into(w, qw):
     if w.numel() != qw.numel:
         raise ValueError(f"w has {w.numel()} elements, the storage holds {qw.numel}")
     _dev(w, w.dtype, "w")
+    _dev_storage(qw)
     _check(fn, getattr(lib(), fn)(_ptr(w), w.numel(), _ptr(qw.codes), _ptr(qw.absmax_fp8), _ptr(qw.superscale),
                                   _stream()))
 
@@ -292,6 +310,7 @@ def nf4_dequantize_dq(qw, out=None, dtype=torch.bfloat16):
         out = torch.empty((qw.N, qw.K), dtype=dtype, device=qw.codes.device)
     fn = "nf4_dequantize_dq" + _ct(out, "out")
     _dev(out, out.dtype, "out")
+    _dev_storage(qw)
     _check(fn, getattr(lib(), fn)(_ptr(qw.codes), _ptr(qw.absmax_fp8), _ptr(qw.superscale), qw.numel, _ptr(out),
                                   _stream()))
     return out
@@ -310,6 +329,7 @@ def _tensor_array(ws, qws):
             raise ValueError(f"tensor {i}: {w.numel()} elements, storage for {qw.numel}")
     for i, (w, qw) in enumerate(zip(ws, qws)):
         _dev(w, torch.bfloat16, "w")
+        _dev_storage(qw)
         arr[i] = NF4Tensor(w.data_ptr(), w.numel(), qw.codes.data_ptr(), qw.absmax_fp8.data_ptr(),
                            qw.superscale.data_ptr())
     return arr
@@ -357,6 +377,7 @@ def nf4_dequantize(qw, out=None):
     if out is None:
         out = torch.empty((qw.N, qw.K), dtype=torch.bfloat16, device=qw.codes.device)
     _dev(out, torch.bfloat16, "out")
+    _dev_storage(qw)
     _check("nf4_dequantize", lib().nf4_dequantize(_ptr(qw.codes), _ptr(qw.absmax), qw.numel, _ptr(out), _stream()))
     return out
 
@@ -379,6 +400,7 @@ def int4_dequantize(qw, out=None):
     if out is None:
         out = torch.empty((qw.N, qw.K), dtype=torch.bfloat16, device=qw.codes.device)
     _dev(out, torch.bfloat16, "out")
+    _dev_storage(qw)
     _check("int4_dequantize", lib().int4_dequantize(_ptr(qw.codes), _ptr(qw.absmax), qw.numel, _ptr(out),
                                                      _stream()))
     return out
@@ -423,6 +445,8 @@ def qlora_linear_fwd(x, qw, lora_a=None, lora_b=None, scaling=1.0, workspace=Non
     _dev(x, x.dtype, "x")
     _dev(lora_a, x.dtype, "lora_a")
     _dev(lora_b, x.dtype, "lora_b")
+    _dev_storage(qw)
+    _dev_workspace(workspace)
     if out is None:
         out = torch.empty((T, qw.N), dtype=x.dtype, device=x.device)
     if workspace is None:
@@ -451,6 +475,7 @@ def qlora_linear_fwd_noalloc(x, qw, lora_a=None, lora_b=None, scaling=1.0, out=N
     _shape(out, (T, qw.N), "out")
     for t, name in ((x, "x"), (lora_a, "lora_a"), (lora_b, "lora_b"), (out, "out")):
         _dev(t, torch.bfloat16, name)
+    _dev_storage(qw)
     if out is None:
         out = torch.empty((T, qw.N), dtype=torch.bfloat16, device=x.device)
     _check("qlora_linear_fwd_noalloc", lib().qlora_linear_fwd_noalloc(
@@ -479,6 +504,7 @@ def _grouped_array(problems, T, r):
         x, qw, a, b, scaling, y = pr
         for t, name in ((x, "x"), (a, "lora_a"), (b, "lora_b"), (y, "out")):
             _dev(t, torch.bfloat16, name)
+        _dev_storage(qw)
         arr[i] = LinearProblem(x.data_ptr(), qw.codes.data_ptr(), qw.absmax_fp8.data_ptr(), qw.superscale.data_ptr(),
                                None if a is None else a.data_ptr(), None if b is None else b.data_ptr(),
                                y.data_ptr(), qw.K, qw.N, float(scaling))
@@ -507,6 +533,7 @@ def qlora_linear_fwd_grouped(problems, workspace=None, product=None):
     T = problems[0][0].shape[0]
     r = 0 if problems[0][2] is None else problems[0][2].shape[1]
     arr = _grouped_array(problems, T, r)
+    _dev_workspace(workspace)
     if workspace is None:
         n = int(lib().qlora_grouped_workspace_bytes(len(problems), arr, T, r))
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=problems[0][0].device)
@@ -549,6 +576,8 @@ def qlora_linear_bwd_input(dy, qw, lora_a=None, lora_b=None, scaling=1.0, x=None
     _dev(x, dy.dtype, "x")
     _dev(lora_a, dy.dtype, "lora_a")
     _dev(lora_b, dy.dtype, "lora_b")
+    _dev_storage(qw)
+    _dev_workspace(workspace)
     if dx is None:
         dx = torch.empty((T, K), dtype=dy.dtype, device=dy.device)
     if lora_grads:
@@ -582,6 +611,7 @@ def qlora_merge_lora(qw, lora_a=None, lora_b=None, scaling=1.0, out=None, dtype=
     _shape(out, (qw.N, qw.K), "out")
     _dev(lora_a, dt, "lora_a")
     _dev(lora_b, dt, "lora_b")
+    _dev_storage(qw)
     if out is None:
         out = torch.empty((qw.N, qw.K), dtype=dt, device=qw.codes.device)
     _dev(out, dt, "out")
@@ -722,6 +752,8 @@ def qlora_linear_act_fwd(x, qw, lora_a=None, lora_b=None, scaling=1.0, bias=None
     _dev(mul, dt, "mul")
     _dev(residual, dt, "residual")
     _dev(out, dt, "out")
+    _dev_storage(qw)
+    _dev_workspace(workspace)
     if out is None:
         out = torch.empty((T, N), dtype=dt, device=x.device)
     z16 = zc = zs = None
@@ -825,6 +857,8 @@ def qlora_linear_act_bwd(dy, qw, lora_a=None, lora_b=None, scaling=1.0, act="non
     for t, name in ((dy, "dy"), (lora_a, "lora_a"), (lora_b, "lora_b"), (dx_add, "dx_add"), (dx, "dx"),
                     (d_lora_a, "d_lora_a"), (d_lora_b, "d_lora_b"), (d_bias, "d_bias"), (d_mul, "d_mul")):
         _dev(t, dt, name)
+    _dev_storage(qw)
+    _dev_workspace(workspace)
     sx, sz, sm = _saved_arg(x, dt, "x"), _saved_arg(z, dt, "z"), _saved_arg(mul, dt, "mul")
     if dx is None:
         dx = torch.empty((T, K), dtype=dt, device=device)
