@@ -28,6 +28,7 @@
 // the kernel's time is set by how many units' latencies overlap, not by any
 // one unit's work, and the third workgroup per CU (over the 64 KB table's
 // two) pays for the extra address instruction per code byte.
+#include <algorithm>
 #include <type_traits>
 
 #include "act.hpp"
@@ -485,18 +486,23 @@ __global__ __launch_bounds__(kWinThreads, G <= 2 ? 4 : 2) void k_gemv_win(GemvGr
 // in registers.  No LDS and no barrier: the B column, the base partials and
 // the first slice partials are all issued before the first sum, so for the
 // decode shapes the kernel waits for one round of loads.
-// CPL columns per lane: 2 up to T = 8, 1 for a 16-token call (more workgroups for
-// its eight waves: 6.4 against 7.2 us), and 1 with one token per wave where the
-// launch has at most 8192 columns (over all its problems), whose 128-column
-// workgroups would be 64 at most (T = 7 on 11008 -> 4096: 21.2 us the launch pair
-// with two columns, 19.8 with one; T = 8 on 4096 -> 11008 the same either way, on
-// 8192 -> 22016 44.1 against 46.9).  The windows of a small prefill take 2 where
+// CPL columns per lane: 1 for a 16-token call (more workgroups for its eight waves:
+// 6.4 against 7.2 us).  Up to T = 8, 2 above 8192 columns (over the launch's
+// problems; T = 8 on 8192 -> 22016 44.1 us the launch pair against 46.9) and, below,
+// where one column would not pay: from T = 5 on while the base partials are one
+// round of a two-token wave (8, K <= 4096: T = 8 on 4096 -> 8192 15.1 against 16.0,
+// on 4096 -> 4096 12.6 against 13.1; with more, T = 7 on 11008 -> 4096 18.5 against
+// 17.7, as one-token waves take 16 a round), and up to T = 4 without an adapter
+// (10.3 against 10.6; with one, whose B columns each wave reads, 11.7 against 11.5).
+// The windows of a small prefill take 2 where
 // 64-column workgroups would be more than one a CU, since each wave reads its lanes'
 // B columns (T = 32 on 4096 -> 11008 10.9 -> 7.5 us, 64 17.3 -> 14.2, 96 25.6 -> 19.9,
 // 96 on 11008 -> 4096 16.3 -> 11.7; with one a CU, 64 on 11008 -> 4096, 9.6 with one
 // column and 10.7 with two).
-constexpr bool fin_wide(int64_t T, int64_t columns, bool windows) {
-    return windows ? columns > 256 * 64 : T <= 8 && columns > 8192;
+constexpr bool fin_wide(int64_t T, int64_t r, int64_t columns, int ks_max, bool windows) {
+    if (windows) return columns > 256 * 64;
+    if (T > 8) return false;
+    return columns > 8192 || (T > 4 ? ks_max <= 8 : r == 0);
 }
 constexpr int fin_cols(bool wide) { return wide ? 128 : 64; }
 //
@@ -763,8 +769,12 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     g.count = count;
     int nl = 0, nbase = 0, nfin = 0;
     int64_t columns = 0;
-    for (int i = 0; i < count; ++i) columns += probs[i].N;
-    const bool wide = fin_wide(T, columns, windows);
+    int ks_max = 0;
+    for (int i = 0; i < count; ++i) {
+        columns += probs[i].N;
+        ks_max = std::max(ks_max, gemv_ks(probs[i].K));
+    }
+    const bool wide = fin_wide(T, r, columns, ks_max, windows);
     for (int i = 0; i < count; ++i) {
         const GemvProblem& q = probs[i];
         GemvArgs& a = g.p[i];
