@@ -378,6 +378,17 @@ __global__ __launch_bounds__(kDecThreads, (DOT || (F16 && TT > 8)) ? 4 : 6) void
 // waves a SIMD at G = 4) and wait for memory at different times.  The k waves are
 // added one window at a time, alternating two 16 KB halves of the table's LDS,
 // one barrier per window.
+//
+// A weight so small that the windows' own k_gemv workgroups are one a CU at most
+// (win_shared is false) has nothing to share: there a workgroup's latency counts,
+// which grows with its windows (six windows of 448 -> 320 without an adapter 12.5 us
+// shared and 10.3 each on its own, of 4096 -> 512 13.3 and 12.0, four of 512 -> 2048
+// 11.5 and 10.8; with more workgroups, six of 1024 -> 4096 13.9 and 14.6).  With an
+// adapter, whose workgroups the launch waits for as well, four windows are no slower
+// shared (2048 -> 1024 14.7 and 15.3).
+constexpr bool win_shared(int count, int64_t N, int ks, int64_t r) {
+    return count < (r > 0 ? 5 : 4) || count * ceil_div(N, kDecRows) * ks > 256;
+}
 constexpr int kWinThreads = 64 * kKW;   // one group of 64 W rows per workgroup
 template <int G, bool SQ, bool F16>
 __global__ __launch_bounds__(kWinThreads, G <= 2 ? 4 : 2) void k_gemv_win(GemvGroup grp, Codebook cb) {
@@ -775,6 +786,7 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
         ks_max = std::max(ks_max, gemv_ks(probs[i].K));
     }
     const bool wide = fin_wide(T, r, columns, ks_max, windows);
+    const bool shared = windows && win_shared(count, probs[0].N, ks_max, r);
     for (int i = 0; i < count; ++i) {
         const GemvProblem& q = probs[i];
         GemvArgs& a = g.p[i];
@@ -795,10 +807,10 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
     const bool sq = probs[0].sc.single();
     if (dot && (sq || f16)) return hipErrorInvalidValue;             // the VALU form serves the bf16 DQ path
     const Codebook& cb = host_codebook();
-    const dim3 grid((unsigned)(nl + (windows ? (int)(probs[0].N / 64) * g.p[0].KS : nbase)));
+    const dim3 grid((unsigned)(nl + (shared ? (int)(probs[0].N / 64) * g.p[0].KS : nbase)));
     hipError_t ae = hipSuccess;
     size_t lds = dot ? kDecLds : (size_t)kNarrowTableBytes;
-    const dim3 threads(windows ? kWinThreads : kDecThreads);
+    const dim3 threads(shared ? kWinThreads : kDecThreads);
     auto go = [&](auto kern) {
         // more than 64 KB of dynamic LDS: above the default limit
         if (lds > 65536)
@@ -823,7 +835,7 @@ hipError_t launch_gemv_group(const GemvProblem* probs, int count, int64_t T, int
         if (sq) f16 ? go(k_gemv_win<G, true, true>) : go(k_gemv_win<G, true, false>);
         else f16 ? go(k_gemv_win<G, false, true>) : go(k_gemv_win<G, false, false>);
     };
-    if (windows) {
+    if (shared) {
         static_assert(kChunkMaxT / kGemvMaxT == 6, "one instance per window count");
         switch (count) {
             case 2: pick_win(std::integral_constant<int, 2>{}); break;
