@@ -344,10 +344,12 @@ int act_fwd_impl(const uint16_t* x, int64_t T, int64_t K, int64_t N, const uint8
 // backward's own regions, then dZ, the partials of both down projections (they
 // run in one launch) and the column-sum partials of the bias gradient.
 //
-// Down projections: up to 16 splits, for about four workgroups a CU over both
-// (each waits for memory most of its time: 4,096 tokens of an 11008 -> 4096
-// layer took 38 us with two a CU).  Adapter gradients: their workgroups hold
-// 128 KB of LDS, one a CU, so both gradients' blocks together take one round.
+// Down projections: up to 16 splits and at most 256 workgroups each, two a CU over
+// both while the splits last.  With 512 each, the whole backward of 2,048 tokens of a
+// 4096 -> 11008 layer took 289 us against 284; at 333, 1,000 and 4,096 tokens the two
+// are equal to 0.5%.  Adapter gradients: their workgroups hold 128 KB of LDS, one a
+// CU, so both gradients' blocks together take one round, up to 256 blocks (ranks
+// above 64 on wide layers have more).
 struct ActBwdPlan {
     ql::LoraPlan pl;
     size_t off_dz, off_gpart, off_ppart, off_part, bytes;

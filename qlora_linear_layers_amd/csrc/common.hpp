@@ -357,9 +357,10 @@ hipError_t launch_dequantize(const uint8_t* codes, BlockScales sc, int64_t numel
 // Forward calls with at most this many tokens take the decode (small-M MFMA) path.
 constexpr int64_t kGemvMaxT = 16;
 // Forward sizes T (kGemvMaxT < T <= kChunkMaxT) that run as kGemvMaxT-token
-// windows of one decode launch pair, which reads and dequantizes the weight once.
-// The seven LLaMA-7B projections (r = 64): 158 us at T = 32, 216 at 64 and 287 at
-// 96, about 36 us a window; the MFMA tiles take 323 us at T = 97 and 313 at 128.
+// windows of one decode launch pair, which reads and dequantizes the weight once
+// (a tiny weight's windows once each).  The seven LLaMA-7B projections (r = 64):
+// 153 us at T = 32, 196 at 64 and 278 at 96, about 31 us a window; the MFMA tiles
+// take 309 us at T = 97 and 298 at 128.
 constexpr int64_t kChunkMaxT = 96;
 struct LoraPlan;
 struct Epilogue;              // output epilogue of the forward (act.hpp); one per problem of a group, or none
