@@ -26,7 +26,8 @@ Sources (titles of the pages, with the part each function follows):
     module docstrings).
 
 The activations, the epilogue, its backward and the 8-bit activation checkpoint
-(``act.py``) come from their own definitions, stated there.
+(``act.py``), and the norm, the 8-bit rows and their product (``block.py``) come from
+their own definitions, stated there.
 
 Parity status: every function is pinned by tests in ``tests/test_oracle_*.py``
 (closed forms, invariants, brute force, library cross-checks); none is
@@ -57,5 +58,6 @@ from .int4 import (
     relative_rms_error,
 )
 from .act import ACTS, CK_BLOCK, act, act_slope, ck_quantize, ck_values, act_fwd, act_bwd
+from .block import ROWS8_PITCH, rows8_quantize, rows8_values, rmsnorm, rmsnorm_bwd, int8_linear
 
 __all__ = [n for n in dir() if not n.startswith("_")]

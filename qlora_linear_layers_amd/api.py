@@ -1,5 +1,5 @@
-"""Thin Python binding over the C ABI of ``libqlora_mi355x.so`` (``include/qlora.h``
-and ``include/qlora_act.h``).
+"""Thin Python binding over the C ABI of ``libqlora_mi355x.so`` (``include/qlora.h``,
+``include/qlora_act.h`` and ``include/qlora_block.h``).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels.  torch provides device memory (tensors) and the current stream.  The
@@ -105,6 +105,17 @@ for _n, _tail in (("qlora_linear_act_fwd", _fwd_tail), ("qlora_linear_act_bwd", 
 for _n in ("act8_quantize", "act8_dequantize", "qlora_linear_act_fwd", "qlora_linear_act_bwd"):
     _SIGS[_n + "_f16"] = _SIGS[_n]
 _SIGS["qlora_act_workspace_bytes_bwd"] = (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64])
+_SIGS["rows8_quantize"] = (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p])
+_SIGS["rows8_dequantize"] = (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p])
+_SIGS["rmsnorm_fwd"] = (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, ctypes.c_int, ctypes.c_float] + [_c_p] * 5)
+_SIGS["rmsnorm_bwd"] = (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, ctypes.c_int, ctypes.c_float] + [_c_p] * 4 +
+                        [ctypes.c_size_t, _c_p])
+_SIGS["int8_linear_fwd"] = (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, ctypes.POINTER(Epilogue),
+                                           _c_p, _c_p, ctypes.c_size_t, _c_p])
+for _n in ("rows8_quantize", "rows8_dequantize", "rmsnorm_fwd", "rmsnorm_bwd", "int8_linear_fwd"):
+    _SIGS[_n + "_f16"] = _SIGS[_n]
+_SIGS["rmsnorm_workspace_bytes_bwd"] = (ctypes.c_size_t, [_c_i64, _c_i64])
+_SIGS["int8_linear_workspace_bytes"] = (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64])
 EXPORTS = tuple(_SIGS)
 
 REUSE_FORWARD = 1   # QLORA_BWD_REUSE_FORWARD
@@ -881,6 +892,237 @@ def qlora_linear_act_bwd(dy, qw, lora_a=None, lora_b=None, scaling=1.0, act="non
         dy.data_ptr(), T, K, N, qw.codes.data_ptr(), *_scale_args(qw)[1], _ptr(lora_a), _ptr(lora_b), r,
         float(scaling), ctypes.byref(g), workspace.data_ptr(), workspace.numel(), _stream()))
     return ActGrads(dx, d_lora_a, d_lora_b, d_bias, d_mul)
+
+
+# ------------------------------------------------------------------ norm, rows in 8 bits, 8-bit integer product
+
+def _one_device(tensors):
+    """Every tensor (None apart) must be on the current device, whose stream the work goes to.
+    Checked after _dev, so all are GPU tensors."""
+    here = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    if t.numel() == 0:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: rows and columns must be at least 1")
+    return t.shape
+
+
+class Rows8:
+    """A matrix in 8 bits with one scale per row (device tensors): `codes` int8 [R, P], rows padded by
+    zeros to the pitch P (rows8_pitch), and `scale` float32 [R]; `shape` is the matrix's (R, K)."""
+    __slots__ = ("codes", "scale", "shape")
+
+    def __init__(self, codes, scale, shape):
+        self.codes, self.scale, self.shape = codes, scale, (int(shape[0]), int(shape[1]))
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.scale.numel()
+
+    def check(self, name):
+        """The tensors must hold exactly what the shape needs: the C ABI trusts the sizes."""
+        R, K = self.shape
+        if R < 1 or K < 1:
+            raise ValueError(f"{name} has shape {self.shape}: rows and columns must be at least 1")
+        _shape(self.codes, (R, rows8_pitch(K)), name + " codes")
+        _shape(self.scale, (R,), name + " scale")
+
+    def dev(self, name):
+        _dev(self.codes, torch.int8, name + " codes")
+        _dev(self.scale, torch.float32, name + " scale")
+
+
+def rows8_pitch(K):
+    """Bytes from one row of codes to the next (QLORA_ROWS8_PITCH)."""
+    return -(-K // 128) * 128
+
+
+def rows8_empty(shape, device="cuda"):
+    """A Rows8 of uninitialised storage for a matrix of `shape` (R, K)."""
+    R, K = shape
+    return Rows8(torch.empty((R, rows8_pitch(K)), dtype=torch.int8, device=device),
+                 torch.empty(R, dtype=torch.float32, device=device), (R, K))
+
+
+def rows8_quantize(x, out=None):
+    """bf16 or fp16 matrix [R, K] (tokens of an activation, or output channels of a weight) -> Rows8
+    (written into `out` if given)."""
+    fn = "rows8_quantize" + _ct(x, "x")
+    R, K = _matrix(x, "x")
+    if out is not None:
+        out.check("out")
+        _shape(x, out.shape, "x")
+        out.dev("out")
+    _dev(x, x.dtype, "x")
+    if out is None:
+        out = rows8_empty((R, K), x.device)
+    _one_device((x, out.codes, out.scale))
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), R, K, out.codes.data_ptr(), out.scale.data_ptr(), _stream()))
+    return out
+
+
+def rows8_dequantize(r8, dtype=torch.bfloat16, out=None):
+    """Rows8 -> the 16-bit values [R, K] it stands for, in `dtype` (or in the dtype of `out`)."""
+    r8.check("rows")
+    _shape(out, r8.shape, "out")
+    r8.dev("rows")
+    if out is None:
+        out = torch.empty(r8.shape, dtype=dtype, device=r8.device)
+    fn = "rows8_dequantize" + _ct(out, "out")
+    _dev(out, out.dtype, "out")
+    _one_device((r8.codes, r8.scale, out))
+    R, K = r8.shape
+    _check(fn, getattr(lib(), fn)(r8.codes.data_ptr(), r8.scale.data_ptr(), R, K, out.data_ptr(), _stream()))
+    return out
+
+
+def _norm_weight(weight, D, dtype):
+    """weight_f32 of a norm's weight [D] in the compute type or float32 (or None)."""
+    if weight is None:
+        return 0
+    _shape(weight, (D,), "weight")
+    if weight.dtype not in (dtype, torch.float32):
+        raise TypeError(f"weight must be {dtype} or torch.float32, got {weight.dtype}")
+    return int(weight.dtype == torch.float32)
+
+
+def rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, quantize=False, keep_h=True, h=None, out=None):
+    """y = h (mean(h^2) + eps)^(-1/2) weight over the rows of h = x + residual, x [T, D] 16-bit; weight
+    [D] in x's dtype or float32, or None for ones.  Returns y, or (y, h) with a residual (`keep_h`
+    False drops h); y is a 16-bit tensor or, with `quantize`, the Rows8 of the unrounded y.  `h` and
+    `out` are written into if given; `h` may be the tensor of x or of residual."""
+    fn = "rmsnorm_fwd" + _ct(x, "x")
+    T, D = _matrix(x, "x")
+    dt = x.dtype
+    w32 = _norm_weight(weight, D, dt)
+    _shape(residual, (T, D), "residual")
+    if h is not None and (residual is None or not keep_h):
+        raise ValueError("h is given but there is no sum to keep")
+    _shape(h, (T, D), "h")
+    if out is not None:
+        if isinstance(out, Rows8) != bool(quantize):
+            raise ValueError("out must be a Rows8 with quantize and a tensor without")
+        if quantize:
+            out.check("out")
+        if tuple(out.shape) != (T, D):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, D)}")
+    _dev(x, dt, "x")
+    _dev(residual, dt, "residual")
+    _dev(h, dt, "h")
+    if weight is not None:
+        _dev(weight, weight.dtype, "weight")
+    if out is None:
+        out = rows8_empty((T, D), x.device) if quantize else torch.empty((T, D), dtype=dt, device=x.device)
+    elif quantize:
+        out.dev("out")
+    else:
+        _dev(out, dt, "out")
+    if residual is not None and keep_h and h is None:
+        h = torch.empty((T, D), dtype=dt, device=x.device)
+    y, yc, ys = (None, out.codes, out.scale) if quantize else (out, None, None)
+    _one_device((x, residual, weight, h, y, yc, ys))
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), _ptr(residual), T, D, _ptr(weight), w32, float(eps), _ptr(h), _ptr(y),
+                                  _ptr(yc), _ptr(ys), _stream()))
+    return out if h is None else (out, h)
+
+
+@dataclass
+class NormGrads:
+    """Gradients of rmsnorm_bwd; d_weight None where not asked for."""
+    dx: torch.Tensor
+    d_weight: torch.Tensor = None
+
+
+def rmsnorm_workspace_bytes_bwd(T, D):
+    return int(lib().rmsnorm_workspace_bytes_bwd(T, D))
+
+
+def rmsnorm_bwd(dy, h, weight=None, eps=1e-6, dx_add=None, weight_grad=True, workspace=None, dx=None, d_weight=None):
+    """Backward of rmsnorm_fwd for upstream gradient dy [T, D] -> NormGrads.  h is what the forward
+    returned (its x without a residual).  dX, the gradient of x and of the residual alike, gets
+    dx_add [T, D] (what reaches h on the residual path) added before its rounding; `dx` may be the
+    tensor of dy or of dx_add.  d_weight [D] in the weight's dtype, when there is a weight and
+    weight_grad."""
+    fn = "rmsnorm_bwd" + _ct(dy, "dy")
+    T, D = _matrix(dy, "dy")
+    dt = dy.dtype
+    _shape(h, (T, D), "h")
+    w32 = _norm_weight(weight, D, dt)
+    weight_grad = weight_grad and weight is not None
+    _shape(dx_add, (T, D), "dx_add")
+    _shape(dx, (T, D), "dx")
+    _grad_out(d_weight, (D,), weight_grad, "d_weight")
+    for t, name in ((dy, "dy"), (h, "h"), (dx_add, "dx_add"), (dx, "dx")):
+        _dev(t, dt, name)
+    if weight is not None:
+        _dev(weight, weight.dtype, "weight")
+        _dev(d_weight, weight.dtype, "d_weight")
+    _dev_workspace(workspace)
+    if dx is None:
+        dx = torch.empty((T, D), dtype=dt, device=dy.device)
+    if weight_grad:
+        if d_weight is None:
+            d_weight = torch.empty((D,), dtype=weight.dtype, device=dy.device)
+        if workspace is None:
+            workspace = torch.empty(max(rmsnorm_workspace_bytes_bwd(T, D), 256), dtype=torch.uint8, device=dy.device)
+    _one_device((dy, h, weight, dx_add, dx, d_weight, workspace))
+    _check(fn, getattr(lib(), fn)(dy.data_ptr(), h.data_ptr(), T, D, _ptr(weight), w32, float(eps), _ptr(dx_add),
+                                  dx.data_ptr(), _ptr(d_weight), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(), _stream()))
+    return NormGrads(dx, d_weight)
+
+
+def int8_linear_workspace_bytes(T, K, N):
+    return int(lib().int8_linear_workspace_bytes(T, K, N))
+
+
+def int8_linear_fwd(x8, w8, dtype=torch.bfloat16, bias=None, act="none", mul=None, residual=None, workspace=None,
+                    out=None):
+    """Y = act(X W^T + bias) * mul + residual of two matrices in 8-bit rows: x8 a Rows8 [T, K] (one scale
+    per token), w8 a Rows8 [N, K] (one per output channel) -> y [T, N] in `dtype` (or in the dtype
+    of `out`).  The product is exact in int32; `act` is one of ACTS; bias [N], mul and residual
+    [T, N] in Y's dtype are left out when None.  `out` may be the tensor of mul or of residual."""
+    code = _act(act)
+    x8.check("x")
+    w8.check("w")
+    (T, K), N = x8.shape, w8.shape[0]
+    if w8.shape[1] != K:
+        raise ValueError(f"w has shape {w8.shape}, expected rows of {K}")
+    _shape(bias, (N,), "bias")
+    _shape(mul, (T, N), "mul")
+    _shape(residual, (T, N), "residual")
+    _shape(out, (T, N), "out")
+    dt = dtype if out is None else out.dtype
+    if dt not in _HALF:
+        raise TypeError(f"out must be bfloat16 or float16, got {dt}")
+    x8.dev("x")
+    w8.dev("w")
+    for t, name in ((bias, "bias"), (mul, "mul"), (residual, "residual"), (out, "out")):
+        _dev(t, dt, name)
+    _dev_workspace(workspace)
+    if out is None:
+        out = torch.empty((T, N), dtype=dt, device=x8.device)
+    L = lib()
+    if workspace is None:
+        n = L.int8_linear_workspace_bytes(T, K, N)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=x8.device)
+    _one_device((x8.codes, x8.scale, w8.codes, w8.scale, bias, mul, residual, out, workspace))
+    ep = Epilogue(code, _ptr(bias), _ptr(mul), _ptr(residual), None, None, None)
+    fn = "int8_linear_fwd_f16" if dt == torch.float16 else "int8_linear_fwd"
+    _check(fn, getattr(L, fn)(
+        x8.codes.data_ptr(), x8.scale.data_ptr(), T, K, N, w8.codes.data_ptr(), w8.scale.data_ptr(), ctypes.byref(ep),
+        out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream()))
+    return out
 
 
 # The _sq entry points under their C names (the wrappers above pick them for an NF4WeightSQ).

@@ -1,0 +1,45 @@
+// The 8-bit integer product: arguments, epilogue and launch.
+#pragma once
+
+#include "act.hpp"
+#include "common.hpp"
+#include "rows.hpp"
+
+namespace ql {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+struct Int8Args {
+    const int8_t* x;          // [T][P]
+    const float* xs;          // [T]
+    const int8_t* w;          // [N][P]
+    const float* ws;          // [N]
+    uint16_t* y;              // [T][N]
+    Epilogue ep;              // z, zc and zs unused
+    int64_t T, N;
+    int P;                    // pitch of a row: K rounded up to 128, zeros past K
+};
+
+// Z = sum dx dw.  The smaller scale first: sum * min stays finite and keeps its
+// bits wherever the result does (a sum of 0 stays 0 where the scales' product
+// would overflow), and a NaN in either scale comes through.
+QL_DEV float int8_scaled(int sum, float xs, float ws) {
+    const bool lt = xs < ws;
+    return ((float)sum * (lt ? xs : ws)) * (lt ? ws : xs);
+}
+
+QL_DEV float act_of(int act, float z) {
+    switch (act) {
+        case kActRelu: return act_value<kActRelu>(z);
+        case kActSilu: return act_value<kActSilu>(z);
+        case kActGelu: return act_value<kActGelu>(z);
+        case kActGeluTanh: return act_value<kActGeluTanh>(z);
+        default: return z;
+    }
+}
+
+size_t int8_workspace(int64_t T, int64_t K, int64_t N);
+hipError_t launch_int8(const Int8Args& a, void* ws, hipStream_t s, bool f16);
+
+}  // namespace ql

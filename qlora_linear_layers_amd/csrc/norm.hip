@@ -1,0 +1,343 @@
+// Root-mean-square norm with the residual's addition, and its backward, for
+// gfx950.  With r = (mean(h^2) + eps)^(-1/2), n = h r and g = dy w:
+//   y  = n w
+//   dx = r (g - n mean(g n)) + dx_add,   dw = sum over rows of dy n
+// (d r / d h_j = -r^3 h_j / D, so the norm's slope takes from g its part along
+// n).  Both are bound by HBM: a row stays in its team's registers (rows.hpp),
+// every input is read once and every output written once.
+#include "rows.hpp"
+
+namespace ql {
+
+namespace {
+
+// Eight weights as they are stored: 16-bit in lo, fp32 in lo and hi, ones
+// without a weight and zeros past the end.
+struct WChunk {
+    u32x4_t lo, hi;
+};
+template <bool F16>
+QL_DEV WChunk weight_load(const void* w, int w32, int c, int D) {
+    WChunk k;
+    const int e0 = c * 8;
+    if (!w) {
+        k.lo = k.hi = u32x4_t{0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u};
+    } else if (!w32) {
+        k.lo = row_load(static_cast<const uint16_t*>(w), c, D);
+        k.hi = u32x4_t{0, 0, 0, 0};
+    } else {
+        const uint32_t* p = static_cast<const uint32_t*>(w) + e0;
+        if (e0 + 8 <= D) {
+            k.lo = *reinterpret_cast<const u32x4_t*>(p);
+            k.hi = *reinterpret_cast<const u32x4_t*>(p + 4);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                k.lo[e] = e0 + e < D ? p[e] : 0u;
+                k.hi[e] = e0 + 4 + e < D ? p[4 + e] : 0u;
+            }
+        }
+    }
+    return k;
+}
+template <bool F16>
+QL_DEV void weight_values(const WChunk& k, bool wide, float (&v)[8]) {
+    if (wide) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = __uint_as_float(k.lo[e]);
+            v[4 + e] = __uint_as_float(k.hi[e]);
+        }
+    } else {
+        unpack8<F16>(k.lo, v);
+    }
+}
+
+// Rows whose squares leave fp32 (rms above 2^64 or so) are summed scaled by this
+// power of two, which eps and the precision do not notice there; the sum of an
+// inf stays inf (r = 0), of a NaN NaN.
+constexpr float kHuge = 0x1p-72f;
+
+QL_DEV float inv_rms(float ss, int D, float eps) { return __builtin_amdgcn_rsqf(ss / (float)D + eps); }
+
+}  // namespace
+
+// y = n w of a row per team.
+template <bool F16, bool Q8, int LANES, int CH>
+__global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
+    __shared__ float slots[2][32];
+    const int lane = (int)threadIdx.x & (LANES - 1), D = a.D;
+    const int64_t row = (int64_t)blockIdx.x * (team_threads(LANES) / LANES) + threadIdx.x / LANES;
+    const bool ok = row < a.T;
+    const int64_t at = (ok ? row : a.T - 1) * D;
+    u32x4_t h[CH];
+    WChunk w[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) h[j] = row_load(a.x + at, lane + j * LANES, D);
+    if (a.res) {
+        u32x4_t q[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) q[j] = row_load(a.res + at, lane + j * LANES, D);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) w[j] = weight_load<F16>(a.w, a.w32, lane + j * LANES, D);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float u[8], v[8];
+            unpack8<F16>(h[j], u);
+            unpack8<F16>(q[j], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] += v[e];
+            h[j] = pack8<F16>(u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) w[j] = weight_load<F16>(a.w, a.w32, lane + j * LANES, D);
+    }
+    if (a.h && ok) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) row_store(a.h + at, lane + j * LANES, D, h[j]);
+    }
+    const auto squares = [&](float pre) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float v[8];
+            unpack8<F16>(h[j], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(v[e] * pre, v[e] * pre, s);
+        }
+        return s;
+    };
+    float pre = 1.0f;
+    float ss = team_sum<LANES>(squares(1.0f), slots[0]);
+    if (!(ss < __builtin_inff())) {                     // the same in the whole team
+        pre = kHuge;
+        if constexpr (LANES > 64) __syncthreads();      // slots[0] is read
+        ss = team_sum<LANES>(squares(pre), slots[0]);
+    }
+    const float r = inv_rms(ss, D, pre == 1.0f ? a.eps : 0.0f);
+    const bool wide = a.w32 || !a.w;
+    const auto normed = [&](int j, float (&y)[8]) {
+        float g[8];
+        unpack8<F16>(h[j], y);
+        weight_values<F16>(w[j], wide, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * pre * r * g[e];
+    };
+    if (a.y && ok) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float y[8];
+            normed(j, y);
+            row_store(a.y + at, lane + j * LANES, D, pack8<F16>(y));
+        }
+    }
+    if constexpr (Q8) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float y[8];
+            normed(j, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if ((lane + j * LANES) * 8 + e < D) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+        }
+        m = team_umax<LANES>(m, slots[1]);
+        float d, inv;
+        rows8_scale(m, d, inv);
+        if (ok) {
+            const int P = (int)rows8_pitch(D);
+            int8_t* cr = a.codes + row * P;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int c = lane + j * LANES;
+                float y[8];
+                normed(j, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = c * 8 + e < D ? y[e] : 0.0f;
+                if (c * 8 < P) *reinterpret_cast<u32x2_t*>(cr + c * 8) = rows8_codes(y, inv);
+            }
+            if (lane == 0) a.scale[row] = d;
+        }
+    }
+}
+
+// dx of a row per team and step, the teams striding over the rows.  A lane holds
+// the same columns of every row, so its share of dw stays in registers and one
+// fp32 partial row per team is written at the end (DW).
+template <bool F16, bool DW, int LANES, int CH>
+__global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, int64_t teams) {
+    __shared__ float slots[2][32];
+    constexpr int kTeams = team_threads(LANES) / LANES;
+    const int lane = (int)threadIdx.x & (LANES - 1), D = a.D;
+    const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / LANES;
+    const bool wide = a.w32 || !a.w;
+    WChunk w[CH];
+    float dw[CH][8];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        w[j] = weight_load<F16>(a.w, a.w32, lane + j * LANES, D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
+    }
+    const float invD = 1.0f / (float)D;
+    int par = 0;
+#pragma unroll 1
+    for (int64_t row = team; row < a.T; row += teams) {
+        const int64_t at = row * D;
+        u32x4_t hq[CH], dyq[CH], aq[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) hq[j] = row_load(a.h + at, lane + j * LANES, D);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) dyq[j] = row_load(a.dy + at, lane + j * LANES, D);
+        if (a.add) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) aq[j] = row_load(a.add + at, lane + j * LANES, D);
+        }
+        const auto sums = [&](float pre, float& ss, float& gh) {
+            ss = gh = 0.0f;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                float h[8], dy[8], g[8];
+                unpack8<F16>(hq[j], h);
+                unpack8<F16>(dyq[j], dy);
+                weight_values<F16>(w[j], wide, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float u = h[e] * pre;
+                    ss = fmaf(u, u, ss);
+                    gh = fmaf(dy[e] * g[e], u, gh);
+                }
+            }
+        };
+        float pre = 1.0f, ss, gh;
+        sums(1.0f, ss, gh);
+        team_sum2<LANES>(ss, gh, slots[par]);
+        if (!(ss < __builtin_inff())) {
+            pre = kHuge;
+            if constexpr (LANES > 64) __syncthreads();
+            sums(pre, ss, gh);
+            team_sum2<LANES>(ss, gh, slots[par]);
+        }
+        par ^= 1;
+        const float r = inv_rms(ss, D, pre == 1.0f ? a.eps : 0.0f);
+        const float m = gh * r * invD;                  // mean(g n)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float h[8], dy[8], g[8];
+            unpack8<F16>(hq[j], h);
+            unpack8<F16>(dyq[j], dy);
+            weight_values<F16>(w[j], wide, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float n = h[e] * pre * r;
+                if constexpr (DW) dw[j][e] = fmaf(dy[e], n, dw[j][e]);
+                h[e] = (dy[e] * g[e] - n * m) * r * pre;
+            }
+            if (a.add) {
+                unpack8<F16>(aq[j], dy);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] += dy[e];
+            }
+            row_store(a.dx + at, lane + j * LANES, D, pack8<F16>(h));
+        }
+    }
+    if constexpr (DW) {
+        if (team < teams) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int e0 = (lane + j * LANES) * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e0 + e < D) a.part[team * D + e0 + e] = dw[j][e];
+            }
+        }
+    }
+}
+
+// dw: 64 columns per workgroup, 16 waves that each add every sixteenth partial;
+// their sums are added in wave order.
+template <bool F16>
+__global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float* __restrict__ part, int64_t teams, int D, int w32,
+                                                     void* __restrict__ dw) {
+    __shared__ float sum[16][64];
+    const int c = (int)blockIdx.x * 64 + ((int)threadIdx.x & 63), wv = (int)threadIdx.x >> 6;
+    float v = 0.0f;
+    if (c < D) {
+#pragma unroll 8
+        for (int64_t q = wv; q < teams; q += 16) v += part[q * D + c];
+    }
+    sum[wv][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (wv == 0 && c < D) {
+#pragma unroll
+        for (int q = 1; q < 16; ++q) v += sum[q][threadIdx.x];
+        if (w32) static_cast<float*>(dw)[c] = v;
+        else static_cast<uint16_t*>(dw)[c] = (uint16_t)(pack16x2<F16>(v, 0.0f) & 0xFFFFu);
+    }
+}
+
+// ------------------------------------------------------------------ launchers
+
+namespace {
+
+// Team of a forward row: one wave up to 2048 values, 256 threads up to 8192, else
+// 1024.
+template <class Go>
+void for_norm_team(int64_t D, Go go) {
+    const int64_t c = ceil_div(D, 8);
+    if (c <= 64) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    else if (c <= 128) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    else if (c <= 256) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+    else if (c <= 512) go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    else if (c <= 1024) go(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    else if (c <= 2048) go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+}
+
+int bwd_lanes(int64_t D) { return D <= 2048 ? 64 : D <= 8192 ? 256 : 1024; }
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s, bool f16) {
+    for_norm_team(a.D, [&](auto lanes, auto ch) {
+        constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
+        const dim3 g((unsigned)ceil_div(a.T, team_threads(L) / L)), b(team_threads(L));
+        if (a.codes) {
+            if (f16) hipLaunchKernelGGL((k_rmsnorm<true, true, L, C>), g, b, 0, s, a);
+            else hipLaunchKernelGGL((k_rmsnorm<false, true, L, C>), g, b, 0, s, a);
+        } else {
+            if (f16) hipLaunchKernelGGL((k_rmsnorm<true, false, L, C>), g, b, 0, s, a);
+            else hipLaunchKernelGGL((k_rmsnorm<false, false, L, C>), g, b, 0, s, a);
+        }
+    });
+    return hipGetLastError();
+}
+
+int64_t rmsnorm_bwd_teams(int64_t T, int64_t D) {
+    const int64_t most = bwd_lanes(D) == 64 ? 1024 : bwd_lanes(D) == 256 ? 512 : 256;
+    return T < most ? T : most;
+}
+
+hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16) {
+    const int64_t teams = rmsnorm_bwd_teams(a.T, a.D);
+    for_norm_team(a.D, [&](auto lanes, auto ch) {
+        constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
+        const dim3 g((unsigned)ceil_div(teams, team_threads(L) / L)), b(team_threads(L));
+        if (a.dw) {
+            if (f16) hipLaunchKernelGGL((k_rmsnorm_bwd<true, true, L, C>), g, b, 0, s, a, teams);
+            else hipLaunchKernelGGL((k_rmsnorm_bwd<false, true, L, C>), g, b, 0, s, a, teams);
+        } else {
+            if (f16) hipLaunchKernelGGL((k_rmsnorm_bwd<true, false, L, C>), g, b, 0, s, a, teams);
+            else hipLaunchKernelGGL((k_rmsnorm_bwd<false, false, L, C>), g, b, 0, s, a, teams);
+        }
+    });
+    if (a.dw) {
+        const dim3 g((unsigned)ceil_div(a.D, 64));
+        if (f16) hipLaunchKernelGGL(k_rmsnorm_dw<true>, g, dim3(1024), 0, s, a.part, teams, a.D, a.w32, a.dw);
+        else hipLaunchKernelGGL(k_rmsnorm_dw<false>, g, dim3(1024), 0, s, a.part, teams, a.D, a.w32, a.dw);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace ql
