@@ -10,6 +10,13 @@ A training forward keeps X, the gate's pre-activation, U and H as checkpoints:
 and gives the gradients of X and of the three adapters; the residual's gradient
 is dY itself.
 
+``NormMlp`` puts the norm in front and the residual stream around the block,
+
+    H = X + R,   Y = H + mlp(norm(H))
+
+and ``Int8Mlp`` serves that block with its adapters merged: the norm writes 8-bit
+rows, and all three products run on 8-bit integers.
+
 The module only orders calls of ``api``; all arithmetic runs in the kernels.
 """
 from dataclasses import dataclass
@@ -87,3 +94,81 @@ class GatedMlp:
         u = api.qlora_linear_act_bwd(g.d_mul, *self.up.args(), x=saved.x, lora_grads=grads(self.up), dx_add=g.dx,
                                      dx=g.dx)
         return MlpGrads(u.dx, (g.d_lora_a, g.d_lora_b), (u.d_lora_a, u.d_lora_b), (d.d_lora_a, d.d_lora_b))
+
+
+@dataclass
+class NormMlpSaved:
+    """What a training forward keeps for the backward."""
+    h: torch.Tensor      # the residual stream in front of the norm, 16 bits
+    mlp: MlpSaved
+
+    def nbytes(self):
+        return self.h.numel() * self.h.element_size() + self.mlp.nbytes()
+
+
+@dataclass
+class NormMlpGrads:
+    dx: torch.Tensor      # of x and of residual alike
+    d_norm: torch.Tensor  # of the norm's weight (None if it is frozen)
+    mlp: MlpGrads
+
+
+class NormMlp:
+    """A GatedMlp behind a root-mean-square norm, with the residual stream around both.
+    norm_weight [D] in the activations' dtype or float32, or None for ones."""
+
+    def __init__(self, mlp, norm_weight=None, eps=1e-6):
+        if norm_weight is not None and tuple(norm_weight.shape) != (mlp.gate.qw.K,):
+            raise ValueError(f"norm_weight has shape {tuple(norm_weight.shape)}, expected {(mlp.gate.qw.K,)}")
+        self.mlp, self.norm_weight, self.eps = mlp, norm_weight, eps
+
+    def _normed(self, x, residual):
+        if residual is None:
+            return api.rmsnorm_fwd(x, self.norm_weight, self.eps), x
+        return api.rmsnorm_fwd(x, self.norm_weight, self.eps, residual=residual)
+
+    def forward(self, x, residual=None):
+        """Y [T, D] of X [T, D] and what is added to it first (the attention's output, say)."""
+        n, h = self._normed(x, residual)
+        return self.mlp.forward(n, residual=h)
+
+    def forward_train(self, x, residual=None):
+        """(Y, NormMlpSaved)"""
+        n, h = self._normed(x, residual)
+        y, saved = self.mlp.forward_train(n, residual=h)
+        return y, NormMlpSaved(h, saved)
+
+    def backward(self, dy, saved, norm_grad=True):
+        """NormMlpGrads for the upstream gradient dY [T, D]."""
+        m = self.mlp.backward(dy, saved.mlp)
+        g = api.rmsnorm_bwd(m.dx, saved.h, self.norm_weight, self.eps, dx_add=dy, weight_grad=norm_grad, dx=m.dx)
+        return NormMlpGrads(g.dx, g.d_weight, m)
+
+
+class Int8Mlp:
+    """A NormMlp for serving, its three weights (Rows8, one scale per output channel) as products of 8-bit
+    integers: gate and up [F, D], down [D, F]."""
+
+    def __init__(self, gate, up, down, norm_weight=None, eps=1e-6, act="silu"):
+        F, D = gate.shape
+        if up.shape != (F, D) or down.shape != (D, F):
+            raise ValueError(f"gate {gate.shape}, up {up.shape} and down {down.shape} do not form a block")
+        if act not in api.ACTS:
+            raise ValueError(f"act must be one of {', '.join(api.ACTS)}, not {act!r}")
+        self.gate, self.up, self.down = gate, up, down
+        self.norm_weight, self.eps, self.act = norm_weight, eps, act
+
+    @classmethod
+    def from_block(cls, block, dtype=torch.bfloat16):
+        """Of a NormMlp: every adapter merged into its weight (in `dtype`), the weight's rows quantized."""
+        rows = (api.rows8_quantize(api.qlora_merge_lora(*layer.args(), dtype=dtype))
+                for layer in (block.mlp.gate, block.mlp.up, block.mlp.down))
+        return cls(*rows, block.norm_weight, block.eps, block.mlp.act)
+
+    def forward(self, x, residual=None):
+        """Y [T, D] of X [T, D] and what is added to it first (prompts and single tokens alike)."""
+        n = api.rmsnorm_fwd(x, self.norm_weight, self.eps, residual=residual, quantize=True)
+        n, h = (n, x) if residual is None else n
+        u = api.int8_linear_fwd(n, self.up, dtype=x.dtype)
+        u = api.int8_linear_fwd(n, self.gate, act=self.act, mul=u, out=u)
+        return api.int8_linear_fwd(api.rows8_quantize(u), self.down, residual=h, dtype=x.dtype)
