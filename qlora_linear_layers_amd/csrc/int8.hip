@@ -34,62 +34,6 @@ QL_DEV uint16_t epi_value(const Int8Args& a, const EpiOperands& o, int sum) {
     return (uint16_t)(pack16x2<F16>(z, 0.0f) & 0xFFFFu);
 }
 
-// Eight channels n .. n + 7 of token t: 16-byte accesses of 2-byte alignment, or
-// element by element where the last of them lie past N.
-struct EpiRow {
-    u32x4_t w0, w1, bias, mul, res;
-    float xs;
-};
-QL_DEV EpiRow epi_row_load(const Int8Args& a, int64_t t, int64_t n) {
-    const int64_t at = t * a.N + n;
-    EpiRow o;
-    o.xs = a.xs[t];
-    o.w0 = *reinterpret_cast<const u32x4_t*>(a.ws + n);
-    o.w1 = *reinterpret_cast<const u32x4_t*>(a.ws + n + 4);
-    o.bias = o.mul = o.res = u32x4_t{0, 0, 0, 0};
-    if (a.ep.bias) o.bias = *reinterpret_cast<const u32x4_t*>(a.ep.bias + n);
-    if (a.ep.mul) o.mul = *reinterpret_cast<const u32x4_a2*>(a.ep.mul + at);
-    if (a.ep.res) o.res = *reinterpret_cast<const u32x4_a2*>(a.ep.res + at);
-    return o;
-}
-template <bool F16>
-QL_DEV void epi_row_store(const Int8Args& a, const EpiRow& o, int64_t t, int64_t n, const int (&sum)[8]) {
-    float v[8], w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = int8_scaled(sum[e], o.xs, __uint_as_float(e < 4 ? o.w0[e] : o.w1[e - 4]));
-    if (a.ep.bias) {
-        unpack8<F16>(o.bias, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w[e];
-    }
-    act_values(a.ep.act, v);
-    if (a.ep.mul) {
-        unpack8<F16>(o.mul, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= w[e];
-    }
-    if (a.ep.res) {
-        unpack8<F16>(o.res, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w[e];
-    }
-    *reinterpret_cast<u32x4_a2*>(a.y + t * a.N + n) = pack8<F16>(v);
-}
-template <bool F16>
-QL_DEV void int8_epilogue8(const Int8Args& a, int64_t t, int64_t n, const int (&sum)[8]) {
-    if (n + 8 <= a.N) {
-        epi_row_store<F16>(a, epi_row_load(a, t, n), t, n, sum);
-    } else {
-#pragma unroll 1
-        for (int e = 0; n + e < a.N; ++e) {
-            int v = sum[0];
-#pragma unroll
-            for (int q = 1; q < 8; ++q) v = e == q ? sum[q] : v;
-            a.y[t * a.N + n + e] = epi_value<F16>(a, epi_load(a, t, n + e), v);
-        }
-    }
-}
-
 // Workgroup -> (channel tile, token tile).  Workgroups are dealt round-robin to
 // the 8 XCDs: each XCD gets a contiguous range of tiles, walked in bands of four
 // token tiles, so that the workgroups that share an L2 share operands.
@@ -103,13 +47,15 @@ QL_DEV void int8_tile_of(int pid, int gn, int gt, int& tn, int& tt) {
     tt = band * kBand + within % bw;
 }
 
-// Scheduling hint of one step: an LDS read behind every MFMA until they are out.
-template <int kMfma, int kReads>
+// Scheduling hint of one step: an LDS read behind every MFMA until they are out,
+// the loads spread over all of them.
+template <int kMfma, int kReads, int kLoads>
 QL_DEV void int8_interleave() {
 #pragma unroll
     for (int j = 0; j < kMfma; ++j) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);               // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // MFMA
         if (j < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // DS read
+        if ((j + 1) * kLoads / kMfma > j * kLoads / kMfma) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // load
     }
 }
 
@@ -165,18 +111,26 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_int8_skinny(Int8Args a) {
 // ------------------------------------------------------------------ tiles
 //
 // BN channels x BM tokens per workgroup of four waves (WN x WM of them), K in
-// tiles of 128 bytes, double-buffered in LDS and filled by loads that go there
-// directly.  LDS rows are 128 bytes with their 16-byte chunks XOR-swizzled
-// (lds_off); a direct load writes 64 consecutive chunks (eight rows), so the
-// swizzle is applied to the chunk that a lane reads from memory.  Rows past N or T
-// repeat the last one (their outputs are not stored).
+// stages of 64 bytes: four stages in LDS, filled by loads that go there directly
+// and run three stages ahead.  A stage's rows are 64 bytes, two to a 128-byte
+// line whose 16-byte chunks are XOR-swizzled by bits of the line (16 consecutive
+// rows at one chunk, which one LDS cycle reads, then lie in all 256 bytes of banks); a direct load writes 64
+// consecutive chunks (16 rows), so the swizzle is applied to the chunk that a lane
+// reads from memory.  Rows past N or T repeat the last one (their outputs are not
+// stored).
 
 typedef __attribute__((address_space(3))) i32x4_t lds_i32x4_t;
+constexpr int kStageK = 64;
+
+QL_DEV uint32_t stage_off(int row, int chunk) {
+    const int line = row >> 1;
+    return (uint32_t)line * 128u + ((uint32_t)(((row & 1) * 4 + chunk) ^ ((line >> 1) & 3)) << 4);
+}
 
 template <int BN, int BM, int WN, int WM>
 struct Int8Tile {
-    static constexpr int kLoads = (BN + BM) / 32;             // direct loads per thread and k tile
-    static constexpr int kStage = (BN + BM) * 128;
+    static constexpr int kLoads = (BN + BM) / 64;             // direct loads per thread and stage
+    static constexpr int kStage = (BN + BM) * kStageK;
     static constexpr int NI = BN / WN / 32, NJ = BM / WM / 32;  // 32 x 32 MFMA tiles of a wave
     rsrc_t rw, rx;
     uint32_t voff[kLoads];
@@ -184,36 +138,51 @@ struct Int8Tile {
 
     QL_DEV void init(const Int8Args& a, int64_t n0, int64_t t0) {
         wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        const int64_t rn = a.N - n0 < BN ? a.N - n0 : BN, rt = a.T - t0 < BM ? a.T - t0 : BM;
+        // 32-bit: scalar units have no 64-bit compare, and a descriptor that goes through
+        // vector registers costs a loop around every load
+        const int rn = min((int)a.N - (int)n0, BN), rt = min((int)a.T - (int)t0, BM);
         rw = make_rsrc(a.w + n0 * a.P, rn * a.P);
         rx = make_rsrc(a.x + t0 * a.P, rt * a.P);
         const int l = (int)threadIdx.x & 63;
+        const int s = (l & 7) ^ ((l >> 4) & 3);               // the lane's chunk: row s >> 2 of its line, chunk s & 3
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int q = (i * 4 + wave) * 8 + (l >> 3);      // row of the stage: W rows, then X rows
-            const int row = i < BN / 32 ? (q < rn ? q : (int)rn - 1) : (q - BN < rt ? q - BN : (int)rt - 1);
-            voff[i] = (uint32_t)row * (uint32_t)a.P + ((uint32_t)((l & 7) ^ ((q ^ (q >> 3)) & 7)) << 4);
+            const int q = (i * 4 + wave) * 16 + (l >> 3) * 2 + (s >> 2);   // row of the stage: W rows, then X rows
+            const int row = i < BN / 64 ? min(q, rn - 1) : min(q - BN, rt - 1);
+            voff[i] = (uint32_t)row * (uint32_t)a.P + (uint32_t)(s & 3) * 16u;
         }
     }
     QL_DEV void load(lds8_t* stage, int kt) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(i < BN / 32 ? rw : rx, stage + (i * 4 + wave) * 1024, 16, voff[i],
-                                                     kt * 128, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(i < BN / 64 ? rw : rx, stage + (i * 4 + wave) * 1024, 16, voff[i],
+                                                     kt * kStageK, 0, 0);
     }
 };
 
 QL_DEV i32x4_t int8_frag(const lds8_t* base, int row, int chunk) {
-    return *reinterpret_cast<const lds_i32x4_t*>(base + lds_off(row, chunk));
+    return *reinterpret_cast<const lds_i32x4_t*>(base + stage_off(row, chunk));
 }
 
-// s0, s1: the two stages, LDS variables of their own, so that the compiler knows
-// that a load into one is no hazard for reads of the other.
-template <bool F16, int BN, int BM, int WN, int WM>
-QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
+// Every wave's wait for all but two stages of its loads and for its LDS reads, then
+// the barrier.  __syncthreads would wait for the loads in flight, too (its fence
+// covers what they write to LDS); the empty asm keeps the compiler from moving
+// memory accesses over the barrier instead.
+template <int kWait>
+QL_DEV void stage_barrier() {
+    __builtin_amdgcn_s_waitcnt(kWait);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// s0 .. s3: the stages, LDS variables of their own, so that the compiler knows
+// that a load into one is no hazard for reads of another.
+template <bool F16, int ACT, int BN, int BM, int WN, int WM>
+QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1, lds8_t* s2, lds8_t* s3) {
     using Tile = Int8Tile<BN, BM, WN, WM>;
     constexpr int NI = Tile::NI, NJ = Tile::NJ;
-    const int gn = (int)ceil_div(a.N, BN), gt = (int)ceil_div(a.T, BM);
+    const int gn = ((int)a.N + BN - 1) / BN, gt = ((int)a.T + BM - 1) / BM;
     int tn, tt;
     int8_tile_of((int)blockIdx.x, gn, gt, tn, tt);
     const int64_t n0 = (int64_t)tn * BN, t0 = (int64_t)tt * BM;
@@ -229,92 +198,178 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-    const int KT = a.P / 128;
+    const int KT = a.P / kStageK;                             // even
 
     i32x4_t fa[2][NI], fb[2][NJ];
-    const auto read = [&](int set, const lds8_t* st, int step) {
+    const auto read = [&](int set, const lds8_t* st) {        // the fragments of 32 K bytes, set = which half of the stage
 #pragma unroll
-        for (int i = 0; i < NI; ++i) fa[set][i] = int8_frag(st, rowa + 32 * i, 2 * step + h);
+        for (int i = 0; i < NI; ++i) fa[set][i] = int8_frag(st, rowa + 32 * i, 2 * set + h);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) fb[set][j] = int8_frag(st, rowb + 32 * j, 2 * step + h);
+        for (int j = 0; j < NJ; ++j) fb[set][j] = int8_frag(st, rowb + 32 * j, 2 * set + h);
     };
     const auto mfma = [&](int set, int j) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
             acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
     };
-    const auto tile = [&](lds8_t* cur, lds8_t* nxt, int kt) {
+    constexpr int kL = Tile::kLoads, kWait = 0x0070 | ((2 * kL) & 15) | ((2 * kL) >> 4) << 14;
+    static_assert(2 * kL < 64, "two stages of loads fit the counter");
+    // One stage: on entry set 0 holds its first half's fragments.  `far` is the stage
+    // read before this one, which the loads three ahead now overwrite.
+    const auto stage = [&](lds8_t* cur, lds8_t* nxt, lds8_t* far, int kt) {
+        tl.load(far, kt + 3 < KT ? kt + 3 : KT - 1);          // past the end: the last one again, which nothing reads
+        read(1, cur);
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
-            read((s + 1) & 1, cur, s + 1);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) mfma(s & 1, j);
-            int8_interleave<NI * NJ, NI + NJ>();
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int j = 0; j < NJ; ++j) mfma(0, j);
+        int8_interleave<NI * NJ, NI + NJ, kL>();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < NJ / 2; ++j) mfma(1, j);
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);                   // vmcnt(0) lgkmcnt(0): the next stage is loaded, this one read
-        __syncthreads();
+        stage_barrier<kWait>();
         __builtin_amdgcn_sched_barrier(0);
-        tl.load(cur, kt + 2 < KT ? kt + 2 : KT - 1);          // past the end: the last one again, which nothing reads
-        read(0, nxt, 0);
+        read(0, nxt);
 #pragma unroll
         for (int j = NJ / 2; j < NJ; ++j) mfma(1, j);
         __builtin_amdgcn_sched_barrier(0);
     };
     tl.load(s0, 0);
-    tl.load(s1, KT > 1 ? 1 : 0);
-    __builtin_amdgcn_s_waitcnt(0x0070);
-    __syncthreads();
-    read(0, s0, 0);
+    tl.load(s1, 1);
+    tl.load(s2, 2 < KT ? 2 : 1);
+    stage_barrier<kWait>();
+    read(0, s0);
     int kt = 0;
 #pragma unroll 1
-    for (; kt + 1 < KT; kt += 2) {
-        tile(s0, s1, kt);
-        tile(s1, s0, kt + 1);
+    for (; kt + 3 < KT; kt += 4) {
+        stage(s0, s1, s3, kt);
+        stage(s1, s2, s0, kt + 1);
+        stage(s2, s3, s1, kt + 2);
+        stage(s3, s0, s2, kt + 3);
     }
-    if (kt < KT) tile(s0, s1, kt);
+    if (kt < KT) {
+        stage(s0, s1, s3, kt);
+        stage(s1, s2, s0, kt + 1);
+    }
 
-    // Epilogue: 32 tokens of every wave at a time through LDS (sums of 32 WM tokens
-    // x BN channels, 4-channel chunks swizzled by the token), then whole rows: eight
-    // channels per thread.
-    constexpr int kRow = BN * 4, kTok = 32 * WM;
-    static_assert(kTok * kRow <= Tile::kStage, "one pass of the epilogue fits a stage");
-    lds8_t* const st = s0;
-    __builtin_amdgcn_s_waitcnt(0x0070);
+    // Epilogue, each wave for itself: 32 tokens at a time through a stage of its own
+    // (sums, 4-channel chunks swizzled by the token), then rows: eight channels per
+    // lane, the same ones for every token, as 16-byte accesses of 2-byte alignment; the
+    // lanes whose last channels lie past N go element by element.  The first operand
+    // (mul, or res) is loaded for the whole wave tile before anything waits: loaded a few
+    // rows at a time, four waves a CU cover too little of the memory latency (the epilogue
+    // of a 256 x 256 tile then took as long as 90 stages).
+    constexpr int kCh = BN / WN, kRow = kCh * 4, kPer = kCh / 8, kItems = 32 * kPer / 64, kStep = 64 / kPer;
+    static_assert(32 * kRow <= Tile::kStage, "32 tokens of a wave fit a stage");
+    lds8_t* const st = tl.wave == 0 ? s0 : tl.wave == 1 ? s1 : tl.wave == 2 ? s2 : s3;
+    const int c8 = lane % kPer, tk0 = lane / kPer, N = (int)a.N;
+    const int n = (int)n0 + wn * kCh + c8 * 8, tw = (int)t0 + wm * (BM / WM), left = (int)a.T - tw;
+    const bool full = n + 8 <= N;
+    // rows of the wave tile: a uniform base and 32-bit byte offsets
+    const int64_t base = (int64_t)tw * N;
+    const auto row8 = [&](const uint16_t* p, int tk) -> const u32x4_a2* {
+        return reinterpret_cast<const u32x4_a2*>(reinterpret_cast<const uint8_t*>(p + base) + ((uint32_t)tk * N + n) * 2u);
+    };
+    const uint16_t* const p1 = a.ep.mul ? a.ep.mul : a.ep.res;
+    const uint16_t* const p2 = a.ep.mul ? a.ep.res : nullptr;
+    __builtin_amdgcn_s_waitcnt(0x0070);                       // the loads past the end have landed, every read is done
+    __syncthreads();
+    u32x4_t q1[NJ][kItems];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int tk = 32 * j + tk0 + u * kStep;
+            q1[j][u] = u32x4_t{0, 0, 0, 0};
+            if (p1 && full && tk < left) q1[j][u] = *row8(p1, tk);
+        }
+    float ws[8], xs[NJ];
+    u32x4_t bias = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ws[e] = n + e < N ? a.ws[n + e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) xs[j] = 32 * j + r < left ? a.xs[tw + 32 * j + r] : 0.0f;
+    if (a.ep.bias && full) bias = *reinterpret_cast<const u32x4_t*>(a.ep.bias + n);
+    const bool edge = (int)n0 + (wn + 1) * kCh > N;              // some lanes are not full
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        __syncthreads();
-        const int tk = wm * 32 + r;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int c = (wn * (BN / WN) + 32 * i + 8 * g + 4 * h) >> 2;
-                *reinterpret_cast<lds_i32x4_t*>(st + tk * kRow + ((c ^ (tk & 31)) << 4)) =
+                const int c = 8 * i + 2 * g + h;
+                *reinterpret_cast<lds_i32x4_t*>(st + r * kRow + ((c ^ (r & (kCh / 4 - 1))) << 4)) =
                     i32x4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
             }
-        __syncthreads();
-#pragma unroll 4
-        for (int u = (int)threadIdx.x; u < kTok * BN / 8; u += 256) {
-            const int tk2 = u / (BN / 8), c8 = u % (BN / 8);
-            const int64_t t = t0 + (tk2 >> 5) * (BM / WM) + 32 * j + (tk2 & 31), n = n0 + c8 * 8;
-            if (t >= a.T || n >= a.N) continue;
-            const i32x4_t lo = *reinterpret_cast<const lds_i32x4_t*>(st + tk2 * kRow + (((2 * c8) ^ (tk2 & 31)) << 4));
-            const i32x4_t hi = *reinterpret_cast<const lds_i32x4_t*>(st + tk2 * kRow + (((2 * c8 + 1) ^ (tk2 & 31)) << 4));
-            const int sum[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            int8_epilogue8<F16>(a, t, n, sum);
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int tk = tk0 + u * kStep, sw = tk & (kCh / 4 - 1);
+            const i32x4_t lo = *reinterpret_cast<const lds_i32x4_t*>(st + tk * kRow + (((2 * c8) ^ sw) << 4));
+            const i32x4_t hi = *reinterpret_cast<const lds_i32x4_t*>(st + tk * kRow + (((2 * c8 + 1) ^ sw) << 4));
+            const float x = __shfl(xs[j], tk);
+            float v[8], w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = int8_scaled(e < 4 ? lo[e] : hi[e - 4], x, ws[e]);
+            if (a.ep.bias) {
+                unpack8<F16>(bias, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += w[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = act_value<ACT>(v[e]);
+            if (p1) {
+                unpack8<F16>(q1[j][u], w);
+                if (a.ep.mul) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= w[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += w[e];
+                }
+            }
+            if (full && 32 * j + tk < left) {
+                if (p2) {
+                    const u32x4_t q2 = *row8(p2, 32 * j + tk);
+                    unpack8<F16>(q2, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += w[e];
+                }
+                *const_cast<u32x4_a2*>(row8(a.y, 32 * j + tk)) = pack8<F16>(v);
+            }
+        }
+        if (edge && !full) {
+#pragma unroll 1
+            for (int tk = tk0; tk < 32 && 32 * j + tk < left; tk += kStep)
+#pragma unroll 1
+                for (int e = 0; n + e < N; ++e) {
+                    const int c = 2 * c8 + (e >> 2);
+                    const int sum = *reinterpret_cast<const __attribute__((address_space(3))) int*>(
+                        st + tk * kRow + ((c ^ (tk & (kCh / 4 - 1))) << 4) + (e & 3) * 4);
+                    const int64_t t = tw + 32 * j + tk;
+                    a.y[t * N + n + e] = epi_value<F16>(a, epi_load(a, t, n + e), sum);
+                }
         }
     }
 }
 
-template <bool F16, int BN, int BM, int WN, int WM>
+template <bool F16, int ACT, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(256) void k_int8_tile(Int8Args a) {
-    __shared__ __align__(1024) uint8_t s0[(BN + BM) * 128];
-    __shared__ __align__(1024) uint8_t s1[(BN + BM) * 128];
-    int8_tile<F16, BN, BM, WN, WM>(a, (lds8_t*)s0, (lds8_t*)s1);
+    constexpr int kStage = (BN + BM) * kStageK;
+    __shared__ __align__(1024) uint8_t s0[kStage], s1[kStage], s2[kStage], s3[kStage];
+    int8_tile<F16, ACT, BN, BM, WN, WM>(a, (lds8_t*)s0, (lds8_t*)s1, (lds8_t*)s2, (lds8_t*)s3);
+}
+
+template <int BN, int BM, int WN, int WM, bool F16>
+void launch_tiles(const Int8Args& a, hipStream_t s) {
+    const dim3 g((unsigned)(ceil_div(a.N, BN) * ceil_div(a.T, BM)));
+    switch (a.ep.act) {
+        case kActRelu: hipLaunchKernelGGL((k_int8_tile<F16, kActRelu, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
+        case kActSilu: hipLaunchKernelGGL((k_int8_tile<F16, kActSilu, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
+        case kActGelu: hipLaunchKernelGGL((k_int8_tile<F16, kActGelu, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
+        case kActGeluTanh:
+            hipLaunchKernelGGL((k_int8_tile<F16, kActGeluTanh, BN, BM, WN, WM>), g, dim3(256), 0, s, a);
+            break;
+        default: hipLaunchKernelGGL((k_int8_tile<F16, kActNone, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
+    }
 }
 
 size_t int8_workspace(int64_t, int64_t, int64_t) { return 0; }
@@ -324,15 +379,11 @@ hipError_t launch_int8(const Int8Args& a, void*, hipStream_t s, bool f16) {
         hipLaunchKernelGGL(kern, dim3((unsigned)ceil_div(a.N, 16), (unsigned)ceil_div(a.T, 16 * nt)),
                            dim3(64 * kSkinnyWaves), 0, s, a);
     };
-    const auto tiles = [&](auto kern, int bn, int bm) {
-        hipLaunchKernelGGL(kern, dim3((unsigned)(ceil_div(a.N, bn) * ceil_div(a.T, bm))), dim3(256), 0, s, a);
-    };
-    if (a.T > 512) {
-        f16 ? tiles(k_int8_tile<true, 256, 256, 2, 2>, 256, 256) : tiles(k_int8_tile<false, 256, 256, 2, 2>, 256, 256);
-        return hipGetLastError();
-    }
     if (a.T > 64) {
-        f16 ? tiles(k_int8_tile<true, 128, 128, 2, 2>, 128, 128) : tiles(k_int8_tile<false, 128, 128, 2, 2>, 128, 128);
+        if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 256)
+            f16 ? launch_tiles<256, 256, 2, 2, true>(a, s) : launch_tiles<256, 256, 2, 2, false>(a, s);
+        else
+            f16 ? launch_tiles<128, 128, 2, 2, true>(a, s) : launch_tiles<128, 128, 2, 2, false>(a, s);
         return hipGetLastError();
     }
     if (a.T <= 16) f16 ? go(k_int8_skinny<true, 1>, 1) : go(k_int8_skinny<false, 1>, 1);
