@@ -47,15 +47,19 @@ QL_DEV void int8_tile_of(int pid, int gn, int gt, int& tn, int& tt) {
     tt = band * kBand + within % bw;
 }
 
-// Scheduling hint of one step: an LDS read behind every MFMA until they are out,
-// the loads spread over all of them.
+// Scheduling hint of kMfma MFMAs: the LDS reads and the loads into LDS spread evenly
+// behind them.
 template <int kMfma, int kReads, int kLoads>
 QL_DEV void int8_interleave() {
 #pragma unroll
     for (int j = 0; j < kMfma; ++j) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // MFMA
-        if (j < kReads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // DS read
-        if ((j + 1) * kLoads / kMfma > j * kLoads / kMfma) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // load
+#pragma unroll
+        for (int q = j * kReads / kMfma; q < (j + 1) * kReads / kMfma; ++q)
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);               // LDS read
+#pragma unroll
+        for (int q = j * kLoads / kMfma; q < (j + 1) * kLoads / kMfma; ++q)
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);               // load
     }
 }
 
@@ -111,26 +115,21 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_int8_skinny(Int8Args a) {
 // ------------------------------------------------------------------ tiles
 //
 // BN channels x BM tokens per workgroup of four waves (WN x WM of them), K in
-// stages of 64 bytes: four stages in LDS, filled by loads that go there directly
-// and run three stages ahead.  A stage's rows are 64 bytes, two to a 128-byte
-// line whose 16-byte chunks are XOR-swizzled by bits of the line (16 consecutive
-// rows at one chunk, which one LDS cycle reads, then lie in all 256 bytes of banks); a direct load writes 64
-// consecutive chunks (16 rows), so the swizzle is applied to the chunk that a lane
-// reads from memory.  Rows past N or T repeat the last one (their outputs are not
-// stored).
+// tiles of 128 bytes, whole cache lines: two buffers in LDS, filled by loads that go
+// there directly.  A wave takes the fragments of a whole K tile into registers during
+// the tile's first quarter, so that its buffer is free from then on and the loads of
+// the tile after next are under way for 1.5 tiles.  LDS rows are 128 bytes with their
+// 16-byte chunks XOR-swizzled (lds_off); a direct load writes 64 consecutive chunks
+// (eight rows), so the swizzle is applied to the chunk that a lane reads from memory.
+// Rows past N or T repeat the last one (their outputs are not stored).
 
 typedef __attribute__((address_space(3))) i32x4_t lds_i32x4_t;
-constexpr int kStageK = 64;
-
-QL_DEV uint32_t stage_off(int row, int chunk) {
-    const int line = row >> 1;
-    return (uint32_t)line * 128u + ((uint32_t)(((row & 1) * 4 + chunk) ^ ((line >> 1) & 3)) << 4);
-}
+constexpr int kTileK = 128;
 
 template <int BN, int BM, int WN, int WM>
 struct Int8Tile {
-    static constexpr int kLoads = (BN + BM) / 64;             // direct loads per thread and stage
-    static constexpr int kStage = (BN + BM) * kStageK;
+    static constexpr int kLoads = (BN + BM) / 32;             // direct loads per thread and K tile
+    static constexpr int kBuf = (BN + BM) * kTileK;
     static constexpr int NI = BN / WN / 32, NJ = BM / WM / 32;  // 32 x 32 MFMA tiles of a wave
     rsrc_t rw, rx;
     uint32_t voff[kLoads];
@@ -144,42 +143,46 @@ struct Int8Tile {
         rw = make_rsrc(a.w + n0 * a.P, rn * a.P);
         rx = make_rsrc(a.x + t0 * a.P, rt * a.P);
         const int l = (int)threadIdx.x & 63;
-        const int s = (l & 7) ^ ((l >> 4) & 3);               // the lane's chunk: row s >> 2 of its line, chunk s & 3
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int q = (i * 4 + wave) * 16 + (l >> 3) * 2 + (s >> 2);   // row of the stage: W rows, then X rows
-            const int row = i < BN / 64 ? min(q, rn - 1) : min(q - BN, rt - 1);
-            voff[i] = (uint32_t)row * (uint32_t)a.P + (uint32_t)(s & 3) * 16u;
+            const int q = (i * 4 + wave) * 8 + (l >> 3);      // row of the buffer: W rows, then X rows
+            const int row = i < BN / 32 ? min(q, rn - 1) : min(q - BN, rt - 1);
+            voff[i] = (uint32_t)row * (uint32_t)a.P + ((uint32_t)((l & 7) ^ ((q ^ (q >> 3)) & 7)) << 4);
         }
     }
-    QL_DEV void load(lds8_t* stage, int kt) const {
+    // loads i0 .. i1 - 1 of K tile kt
+    QL_DEV void load(lds8_t* buf, int kt, int i0, int i1) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(i < BN / 64 ? rw : rx, stage + (i * 4 + wave) * 1024, 16, voff[i],
-                                                     kt * kStageK, 0, 0);
+            if (i >= i0 && i < i1)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(i < BN / 32 ? rw : rx, buf + (i * 4 + wave) * 1024, 16,
+                                                         voff[i], kt * kTileK, 0, 0);
     }
 };
 
 QL_DEV i32x4_t int8_frag(const lds8_t* base, int row, int chunk) {
-    return *reinterpret_cast<const lds_i32x4_t*>(base + stage_off(row, chunk));
+    return *reinterpret_cast<const lds_i32x4_t*>(base + lds_off(row, chunk));
 }
 
-// Every wave's wait for all but two stages of its loads and for its LDS reads, then
-// the barrier.  __syncthreads would wait for the loads in flight, too (its fence
-// covers what they write to LDS); the empty asm keeps the compiler from moving
-// memory accesses over the barrier instead.
+// A wave's own wait, then the barrier.  __syncthreads would wait for the loads in
+// flight, too (its fence covers what they write to LDS); the empty asm keeps the
+// compiler from moving memory accesses over the barrier instead.
 template <int kWait>
-QL_DEV void stage_barrier() {
+QL_DEV void wait_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(kWait);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
+constexpr int kWaitLds = 0xC07F;                               // lgkmcnt(0)
+constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }   // vmcnt(n)
 
-// s0 .. s3: the stages, LDS variables of their own, so that the compiler knows
-// that a load into one is no hazard for reads of another.
+// s0, s1: the buffers, LDS variables of their own, so that the compiler knows that a
+// load into one is no hazard for reads of the other.
 template <bool F16, int ACT, int BN, int BM, int WN, int WM>
-QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1, lds8_t* s2, lds8_t* s3) {
+QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
     using Tile = Int8Tile<BN, BM, WN, WM>;
     constexpr int NI = Tile::NI, NJ = Tile::NJ;
     const int gn = ((int)a.N + BN - 1) / BN, gt = ((int)a.T + BM - 1) / BM;
@@ -198,69 +201,70 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1, lds8_t* s2, lds
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-    const int KT = a.P / kStageK;                             // even
+    const int KT = a.P / kTileK;
 
-    i32x4_t fa[2][NI], fb[2][NJ];
-    const auto read = [&](int set, const lds8_t* st) {        // the fragments of 32 K bytes, set = which half of the stage
+    i32x4_t fa[4][NI], fb[4][NJ];                             // of the four steps of 32 K bytes
+    const auto read = [&](int s, const lds8_t* buf) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) fa[set][i] = int8_frag(st, rowa + 32 * i, 2 * set + h);
+        for (int j = 0; j < NJ; ++j) fb[s][j] = int8_frag(buf, rowb + 32 * j, 2 * s + h);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) fb[set][j] = int8_frag(st, rowb + 32 * j, 2 * set + h);
+        for (int i = 0; i < NI; ++i) fa[s][i] = int8_frag(buf, rowa + 32 * i, 2 * s + h);
     };
-    const auto mfma = [&](int set, int j) {
+    const auto mfma = [&](int s, int j0, int j1) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < NJ; ++j)
+            if (j >= j0 && j < j1)
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[s][i], fb[s][j], acc[i][j], 0, 0, 0);
     };
-    constexpr int kL = Tile::kLoads, kWait = 0x0070 | ((2 * kL) & 15) | ((2 * kL) >> 4) << 14;
-    static_assert(2 * kL < 64, "two stages of loads fit the counter");
-    // One stage: on entry set 0 holds its first half's fragments.  `far` is the stage
-    // read before this one, which the loads three ahead now overwrite.
-    const auto stage = [&](lds8_t* cur, lds8_t* nxt, lds8_t* far, int kt) {
-        tl.load(far, kt + 3 < KT ? kt + 3 : KT - 1);          // past the end: the last one again, which nothing reads
+    constexpr int kL = Tile::kLoads, kF = NI + NJ, kM = NI * NJ, kEarly = kL / 3;
+    // One K tile: on entry step 0's fragments are read.
+    const auto tile = [&](lds8_t* cur, lds8_t* nxt, int kt) {
+        const int ahead = kt + 2 < KT ? kt + 2 : KT - 1;      // past the end: the last one again, which nothing reads
         read(1, cur);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) mfma(0, j);
-        int8_interleave<NI * NJ, NI + NJ, kL>();
+        read(2, cur);
+        read(3, cur);
+        mfma(0, 0, NJ);
+        int8_interleave<kM, 3 * kF, 0>();
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < NJ / 2; ++j) mfma(1, j);
+        mfma(1, 0, NJ / 2);
+        wait_barrier<kWaitLds>();                             // everyone has read all of cur
+        tl.load(cur, ahead, 0, kEarly);
+        mfma(1, NJ / 2, NJ);
+        int8_interleave<kM / 2, 0, kEarly>();
         __builtin_amdgcn_sched_barrier(0);
-        stage_barrier<kWait>();
-        __builtin_amdgcn_sched_barrier(0);
+        tl.load(cur, ahead, kEarly, kL);
+        mfma(2, 0, NJ);
+        int8_interleave<kM, 0, kL - kEarly>();
+        wait_barrier<wait_loads(kL)>();                       // nxt has landed, the loads just issued may fly
         read(0, nxt);
-#pragma unroll
-        for (int j = NJ / 2; j < NJ; ++j) mfma(1, j);
+        mfma(3, 0, NJ);
+        int8_interleave<kM, kF, 0>();
         __builtin_amdgcn_sched_barrier(0);
     };
-    tl.load(s0, 0);
-    tl.load(s1, 1);
-    tl.load(s2, 2 < KT ? 2 : 1);
-    stage_barrier<kWait>();
+    tl.load(s0, 0, 0, kL);
+    tl.load(s1, KT > 1 ? 1 : 0, 0, kL);
+    wait_barrier<wait_loads(kL)>();
     read(0, s0);
     int kt = 0;
 #pragma unroll 1
-    for (; kt + 3 < KT; kt += 4) {
-        stage(s0, s1, s3, kt);
-        stage(s1, s2, s0, kt + 1);
-        stage(s2, s3, s1, kt + 2);
-        stage(s3, s0, s2, kt + 3);
+    for (; kt + 1 < KT; kt += 2) {
+        tile(s0, s1, kt);
+        tile(s1, s0, kt + 1);
     }
-    if (kt < KT) {
-        stage(s0, s1, s3, kt);
-        stage(s1, s2, s0, kt + 1);
-    }
+    if (kt < KT) tile(s0, s1, kt);
 
-    // Epilogue, each wave for itself: 32 tokens at a time through a stage of its own
+    // Epilogue, each wave for itself: 32 tokens at a time through LDS of its own
     // (sums, 4-channel chunks swizzled by the token), then rows: eight channels per
     // lane, the same ones for every token, as 16-byte accesses of 2-byte alignment; the
     // lanes whose last channels lie past N go element by element.  The first operand
     // (mul, or res) is loaded for the whole wave tile before anything waits: loaded a few
     // rows at a time, four waves a CU cover too little of the memory latency (the epilogue
-    // of a 256 x 256 tile then took as long as 90 stages).
+    // of a 256 x 256 tile then took as long as 45 K tiles).
     constexpr int kCh = BN / WN, kRow = kCh * 4, kPer = kCh / 8, kItems = 32 * kPer / 64, kStep = 64 / kPer;
-    static_assert(32 * kRow <= Tile::kStage, "32 tokens of a wave fit a stage");
-    lds8_t* const st = tl.wave == 0 ? s0 : tl.wave == 1 ? s1 : tl.wave == 2 ? s2 : s3;
+    static_assert(64 * kRow <= Tile::kBuf, "32 tokens of two waves fit a buffer");
+    lds8_t* const st = (tl.wave < 2 ? s0 : s1) + (tl.wave & 1) * 32 * kRow;
     const int c8 = lane % kPer, tk0 = lane / kPer, N = (int)a.N;
     const int n = (int)n0 + wn * kCh + c8 * 8, tw = (int)t0 + wm * (BM / WM), left = (int)a.T - tw;
     const bool full = n + 8 <= N;
@@ -353,9 +357,8 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1, lds8_t* s2, lds
 
 template <bool F16, int ACT, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(256) void k_int8_tile(Int8Args a) {
-    constexpr int kStage = (BN + BM) * kStageK;
-    __shared__ __align__(1024) uint8_t s0[kStage], s1[kStage], s2[kStage], s3[kStage];
-    int8_tile<F16, ACT, BN, BM, WN, WM>(a, (lds8_t*)s0, (lds8_t*)s1, (lds8_t*)s2, (lds8_t*)s3);
+    __shared__ __align__(1024) uint8_t s0[(BN + BM) * kTileK], s1[(BN + BM) * kTileK];
+    int8_tile<F16, ACT, BN, BM, WN, WM>(a, (lds8_t*)s0, (lds8_t*)s1);
 }
 
 template <int BN, int BM, int WN, int WM, bool F16>
