@@ -10,19 +10,17 @@ template <bool F16>
 QL_DEV float value16(uint16_t v) { return lo16<F16>(v); }
 
 // Output (t, n): what the epilogue reads, loaded ahead, and the rounding at the end.
+// The loads have no branches (a missing operand is read from the weight's scales and
+// not used), so that nothing waits for them until the end.
 struct EpiOperands {
     float xs, ws;
     uint16_t bias, mul, res;
 };
 QL_DEV EpiOperands epi_load(const Int8Args& a, int64_t t, int64_t n) {
     const int64_t at = t * a.N + n;
-    EpiOperands o;
-    o.xs = a.xs[t];
-    o.ws = a.ws[n];
-    o.bias = a.ep.bias ? a.ep.bias[n] : 0;
-    o.mul = a.ep.mul ? a.ep.mul[at] : 0;
-    o.res = a.ep.res ? a.ep.res[at] : 0;
-    return o;
+    const uint16_t* const none = reinterpret_cast<const uint16_t*>(a.ws);
+    return {a.xs[t], a.ws[n], *(a.ep.bias ? a.ep.bias + n : none), *(a.ep.mul ? a.ep.mul + at : none),
+            *(a.ep.res ? a.ep.res + at : none)};
 }
 template <bool F16>
 QL_DEV uint16_t epi_value(const Int8Args& a, const EpiOperands& o, int sum) {
@@ -63,62 +61,95 @@ QL_DEV void int8_interleave() {
     }
 }
 
-constexpr int kSkinnyWaves = 8;
-
 }  // namespace
 
-// 16 NT tokens x 16 channels per workgroup, K split over its eight waves in
-// steps of 128 bytes; the waves' sums are added in LDS.
-template <bool F16, int NT>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void k_int8_skinny(Int8Args a) {
-    __shared__ int sums[kSkinnyWaves][NT][16][16];
-    const int lane = (int)threadIdx.x & 63, wv = (int)threadIdx.x >> 6;
+// 16 NT tokens x 16 channels per workgroup, K dealt to its WAVES waves in steps of
+// 128 bytes (neighbouring waves read neighbouring steps), whose sums are added in LDS.
+// A wave keeps the loads of D steps in flight; what the epilogue reads is loaded first
+// of all, so that its latency passes meanwhile.
+template <bool F16, int NT, int WAVES, int D>
+__global__ __launch_bounds__(64 * WAVES) void k_int8_skinny(Int8Args a) {
+    constexpr int kThreads = 64 * WAVES, kOut = (NT * 256 + kThreads - 1) / kThreads;
+    __shared__ int sums[WAVES][NT][16][16];
+    const int lane = (int)threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * (16 * NT);
-    const int64_t n = n0 + l16 < a.N ? n0 + l16 : a.N - 1;
-    const int8_t* wr = a.w + n * a.P + g * 16;
+    const int n0 = (int)blockIdx.x * 16, t0 = (int)blockIdx.y * (16 * NT), N = (int)a.N, T = (int)a.T;
+    EpiOperands op[kOut];
+#pragma unroll
+    for (int q = 0; q < kOut; ++q) {
+        const int e = (int)threadIdx.x + q * kThreads;
+        op[q] = epi_load(a, min(t0 + e / 16, T - 1), min(n0 + e % 16, N - 1));
+    }
+    const int8_t* wr = a.w + (int64_t)min(n0 + l16, N - 1) * a.P + g * 16;
     const int8_t* xr[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int64_t t = t0 + 16 * i + l16;
-        xr[i] = a.x + (t < a.T ? t : a.T - 1) * a.P + g * 16;
-    }
-    i32x4_t acc[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = i32x4_t{0, 0, 0, 0};
-    for (int k = wv * 128; k < a.P; k += 128 * kSkinnyWaves) {
+    for (int i = 0; i < NT; ++i) xr[i] = a.x + (int64_t)min(t0 + 16 * i + l16, T - 1) * a.P + g * 16;
+    const int steps = a.P / 128;
+    i32x4_t wf[D][2], xf[D][2][NT], acc[NT];
+    const auto load = [&](int u, int s) {
+        const int k = s * 128;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const i32x4_t wf = *reinterpret_cast<const i32x4_t*>(wr + k + 64 * j);
+            wf[u][j] = *reinterpret_cast<const i32x4_t*>(wr + k + 64 * j);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) xf[u][j][i] = *reinterpret_cast<const i32x4_t*>(xr[i] + k + 64 * j);
+        }
+        asm volatile("" ::: "memory");                        // loads stay here, they do not sink to their uses
+    };
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = i32x4_t{0, 0, 0, 0};
+    const auto mul = [&](int u) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4_t*>(xr[i] + k + 64 * j), wf,
-                                                               acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xf[u][j][i], wf[u][j], acc[i], 0, 0, 0);
+    };
+#pragma unroll
+    for (int u = 0; u < D; ++u) load(u, min(wv + u * WAVES, steps - 1));   // past the end: the last step again, not multiplied
+    int s = wv;
+#pragma unroll 1
+    for (; s + (2 * D - 1) * WAVES < steps; s += D * WAVES)
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+            mul(u);
+            load(u, s + (u + D) * WAVES);
         }
-    }
+    // fewer than 2 D steps are left, the first D of them loaded
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+        if (s + u * WAVES < steps) {
+            mul(u);
+            if (s + (u + D) * WAVES < steps) load(u, s + (u + D) * WAVES);
+        }
+#pragma unroll
+    for (int u = 0; u < D - 1; ++u)
+        if (s + (u + D) * WAVES < steps) mul(u);
     // lane holds tokens 4 g .. 4 g + 3 of channel l16
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) sums[wv][i][4 * g + q][l16] = acc[i][q];
     __syncthreads();
-    for (int e = (int)threadIdx.x; e < NT * 256; e += 64 * kSkinnyWaves) {
-        const int64_t t = t0 + e / 16, nn = n0 + e % 16;
-        if (t >= a.T || nn >= a.N) continue;
+#pragma unroll
+    for (int q = 0; q < kOut; ++q) {
+        const int e = (int)threadIdx.x + q * kThreads;
+        const int t = t0 + e / 16, n = n0 + e % 16;
+        if (e >= NT * 256 || t >= T || n >= N) continue;
         int v = 0;
 #pragma unroll
-        for (int w = 0; w < kSkinnyWaves; ++w) v += sums[w][e / 256][e / 16 % 16][e % 16];
-        a.y[t * a.N + nn] = epi_value<F16>(a, epi_load(a, t, nn), v);
+        for (int w = 0; w < WAVES; ++w) v += sums[w][e / 256][e / 16 % 16][e % 16];
+        a.y[(int64_t)t * N + n] = epi_value<F16>(a, op[q], v);
     }
 }
 
 // ------------------------------------------------------------------ tiles
 //
 // BN channels x BM tokens per workgroup of four waves (WN x WM of them), K in
-// tiles of 128 bytes, whole cache lines: two buffers in LDS, filled by loads that go
+// tiles of 128 bytes, whole cache lines: S buffers in LDS, filled by loads that go
 // there directly.  A wave takes the fragments of a whole K tile into registers during
-// the tile's first quarter, so that its buffer is free from then on and the loads of
-// the tile after next are under way for 1.5 tiles.  LDS rows are 128 bytes with their
+// the tile's first quarter, so that its buffer is free from then on and the loads S
+// tiles ahead are under way for S - 1/2 tiles.  LDS rows are 128 bytes with their
 // 16-byte chunks XOR-swizzled (lds_off); a direct load writes 64 consecutive chunks
 // (eight rows), so the swizzle is applied to the chunk that a lane reads from memory.
 // Rows past N or T repeat the last one (their outputs are not stored).
@@ -179,10 +210,10 @@ QL_DEV void wait_barrier() {
 constexpr int kWaitLds = 0xC07F;                               // lgkmcnt(0)
 constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }   // vmcnt(n)
 
-// s0, s1: the buffers, LDS variables of their own, so that the compiler knows that a
-// load into one is no hazard for reads of the other.
-template <bool F16, int ACT, int BN, int BM, int WN, int WM>
-QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
+// buf: the S buffers, LDS variables of their own, so that the compiler knows that a
+// load into one is no hazard for reads of another.
+template <bool F16, int ACT, int BN, int BM, int WN, int WM, int S>
+QL_DEV void int8_tile(const Int8Args& a, lds8_t* const (&buf)[S]) {
     using Tile = Int8Tile<BN, BM, WN, WM>;
     constexpr int NI = Tile::NI, NJ = Tile::NJ;
     const int gn = ((int)a.N + BN - 1) / BN, gt = ((int)a.T + BM - 1) / BM;
@@ -218,10 +249,15 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
                 for (int i = 0; i < NI; ++i)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[s][i], fb[s][j], acc[i][j], 0, 0, 0);
     };
-    constexpr int kL = Tile::kLoads, kF = NI + NJ, kM = NI * NJ, kEarly = kL / 3;
+    constexpr int kL = Tile::kLoads, kF = NI + NJ, kM = NI * NJ;
+    // Loads issued by the end of steps 1 and 2.  With 16 MFMAs a step the loads keep the
+    // address unit half busy, and a wave that waits for it cannot issue MFMAs: they are
+    // spread to the tile's end (2048 tokens through 8192 -> 22016 334 us, against 358 with
+    // all of them by the end of step 2).
+    constexpr int kL1 = kM >= 16 ? kL / 5 : kL / 3, kL2 = kM >= 16 ? 3 * kL / 5 : kL;
     // One K tile: on entry step 0's fragments are read.
     const auto tile = [&](lds8_t* cur, lds8_t* nxt, int kt) {
-        const int ahead = kt + 2 < KT ? kt + 2 : KT - 1;      // past the end: the last one again, which nothing reads
+        const int ahead = kt + S < KT ? kt + S : KT - 1;      // past the end: the last one again, which nothing reads
         read(1, cur);
         read(2, cur);
         read(3, cur);
@@ -230,30 +266,33 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
         __builtin_amdgcn_sched_barrier(0);
         mfma(1, 0, NJ / 2);
         wait_barrier<kWaitLds>();                             // everyone has read all of cur
-        tl.load(cur, ahead, 0, kEarly);
+        tl.load(cur, ahead, 0, kL1);
         mfma(1, NJ / 2, NJ);
-        int8_interleave<kM / 2, 0, kEarly>();
+        int8_interleave<kM / 2, 0, kL1>();
         __builtin_amdgcn_sched_barrier(0);
-        tl.load(cur, ahead, kEarly, kL);
+        tl.load(cur, ahead, kL1, kL2);
         mfma(2, 0, NJ);
-        int8_interleave<kM, 0, kL - kEarly>();
-        wait_barrier<wait_loads(kL)>();                       // nxt has landed, the loads just issued may fly
+        int8_interleave<kM, 0, kL2 - kL1>();
+        wait_barrier<wait_loads((S - 2) * kL + kL2)>();       // nxt has landed, the later tiles' loads may fly
         read(0, nxt);
+        tl.load(cur, ahead, kL2, kL);
         mfma(3, 0, NJ);
-        int8_interleave<kM, kF, 0>();
+        int8_interleave<kM, kF, kL - kL2>();
         __builtin_amdgcn_sched_barrier(0);
     };
-    tl.load(s0, 0, 0, kL);
-    tl.load(s1, KT > 1 ? 1 : 0, 0, kL);
-    wait_barrier<wait_loads(kL)>();
-    read(0, s0);
+    static_assert((S - 1) * kL < 64, "the loads in flight fit the counter");
+#pragma unroll
+    for (int q = 0; q < S; ++q) tl.load(buf[q], q < KT ? q : KT - 1, 0, kL);
+    wait_barrier<wait_loads((S - 1) * kL)>();
+    read(0, buf[0]);
     int kt = 0;
 #pragma unroll 1
-    for (; kt + 1 < KT; kt += 2) {
-        tile(s0, s1, kt);
-        tile(s1, s0, kt + 1);
-    }
-    if (kt < KT) tile(s0, s1, kt);
+    for (; kt + S <= KT; kt += S)
+#pragma unroll
+        for (int q = 0; q < S; ++q) tile(buf[q], buf[(q + 1) % S], kt + q);
+#pragma unroll
+    for (int q = 0; q < S - 1; ++q)
+        if (kt + q < KT) tile(buf[q], buf[q + 1], kt + q);
 
     // Epilogue, each wave for itself: 32 tokens at a time through LDS of its own
     // (sums, 4-channel chunks swizzled by the token), then rows: eight channels per
@@ -264,7 +303,7 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
     // of a 256 x 256 tile then took as long as 45 K tiles).
     constexpr int kCh = BN / WN, kRow = kCh * 4, kPer = kCh / 8, kItems = 32 * kPer / 64, kStep = 64 / kPer;
     static_assert(64 * kRow <= Tile::kBuf, "32 tokens of two waves fit a buffer");
-    lds8_t* const st = (tl.wave < 2 ? s0 : s1) + (tl.wave & 1) * 32 * kRow;
+    lds8_t* const st = (tl.wave < 2 ? buf[0] : buf[1]) + (tl.wave & 1) * 32 * kRow;
     const int c8 = lane % kPer, tk0 = lane / kPer, N = (int)a.N;
     const int n = (int)n0 + wn * kCh + c8 * 8, tw = (int)t0 + wm * (BM / WM), left = (int)a.T - tw;
     const bool full = n + 8 <= N;
@@ -355,43 +394,58 @@ QL_DEV void int8_tile(const Int8Args& a, lds8_t* s0, lds8_t* s1) {
     }
 }
 
-template <bool F16, int ACT, int BN, int BM, int WN, int WM>
+template <bool F16, int ACT, int BN, int BM, int WN, int WM, int S>
 __global__ __launch_bounds__(256) void k_int8_tile(Int8Args a) {
-    __shared__ __align__(1024) uint8_t s0[(BN + BM) * kTileK], s1[(BN + BM) * kTileK];
-    int8_tile<F16, ACT, BN, BM, WN, WM>(a, (lds8_t*)s0, (lds8_t*)s1);
+    constexpr int kBuf = (BN + BM) * kTileK;
+    __shared__ __align__(1024) uint8_t s0[kBuf], s1[kBuf];
+    if constexpr (S == 4) {
+        __shared__ __align__(1024) uint8_t s2[kBuf], s3[kBuf];
+        int8_tile<F16, ACT, BN, BM, WN, WM, 4>(a, {(lds8_t*)s0, (lds8_t*)s1, (lds8_t*)s2, (lds8_t*)s3});
+    } else {
+        int8_tile<F16, ACT, BN, BM, WN, WM, 2>(a, {(lds8_t*)s0, (lds8_t*)s1});
+    }
 }
 
-template <int BN, int BM, int WN, int WM, bool F16>
+template <int BN, int BM, int WN, int WM, int S, bool F16>
 void launch_tiles(const Int8Args& a, hipStream_t s) {
     const dim3 g((unsigned)(ceil_div(a.N, BN) * ceil_div(a.T, BM)));
+    const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, g, dim3(256), 0, s, a); };
     switch (a.ep.act) {
-        case kActRelu: hipLaunchKernelGGL((k_int8_tile<F16, kActRelu, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
-        case kActSilu: hipLaunchKernelGGL((k_int8_tile<F16, kActSilu, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
-        case kActGelu: hipLaunchKernelGGL((k_int8_tile<F16, kActGelu, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
-        case kActGeluTanh:
-            hipLaunchKernelGGL((k_int8_tile<F16, kActGeluTanh, BN, BM, WN, WM>), g, dim3(256), 0, s, a);
-            break;
-        default: hipLaunchKernelGGL((k_int8_tile<F16, kActNone, BN, BM, WN, WM>), g, dim3(256), 0, s, a); break;
+        case kActRelu: go(k_int8_tile<F16, kActRelu, BN, BM, WN, WM, S>); break;
+        case kActSilu: go(k_int8_tile<F16, kActSilu, BN, BM, WN, WM, S>); break;
+        case kActGelu: go(k_int8_tile<F16, kActGelu, BN, BM, WN, WM, S>); break;
+        case kActGeluTanh: go(k_int8_tile<F16, kActGeluTanh, BN, BM, WN, WM, S>); break;
+        default: go(k_int8_tile<F16, kActNone, BN, BM, WN, WM, S>); break;
     }
 }
 
 size_t int8_workspace(int64_t, int64_t, int64_t) { return 0; }
 
-hipError_t launch_int8(const Int8Args& a, void*, hipStream_t s, bool f16) {
-    const auto go = [&](auto kern, int nt) {
-        hipLaunchKernelGGL(kern, dim3((unsigned)ceil_div(a.N, 16), (unsigned)ceil_div(a.T, 16 * nt)),
-                           dim3(64 * kSkinnyWaves), 0, s, a);
+template <bool F16>
+static hipError_t launch_int8_of(const Int8Args& a, hipStream_t s) {
+    const auto skinny = [&](auto kern, int nt, int waves) {
+        hipLaunchKernelGGL(kern, dim3((unsigned)ceil_div(a.N, 16), (unsigned)ceil_div(a.T, 16 * nt)), dim3(64 * waves), 0,
+                           s, a);
     };
-    if (a.T > 64) {
-        if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 256)
-            f16 ? launch_tiles<256, 256, 2, 2, true>(a, s) : launch_tiles<256, 256, 2, 2, false>(a, s);
-        else
-            f16 ? launch_tiles<128, 128, 2, 2, true>(a, s) : launch_tiles<128, 128, 2, 2, false>(a, s);
-        return hipGetLastError();
+    if (a.T <= 16) {
+        if (a.P <= 4096) skinny(k_int8_skinny<F16, 1, 8, 4>, 1, 8);
+        else skinny(k_int8_skinny<F16, 1, 16, 4>, 1, 16);
+    } else if (a.T <= 32) {
+        skinny(k_int8_skinny<F16, 2, 8, 4>, 2, 8);
+    } else if (a.T <= 64) {
+        skinny(k_int8_skinny<F16, 4, 8, 3>, 4, 8);
+    } else if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 256) {
+        launch_tiles<256, 256, 2, 2, 2, F16>(a, s);
+    } else if (ceil_div(a.N, 128) * ceil_div(a.T, 128) > 256) {
+        launch_tiles<128, 128, 2, 2, 2, F16>(a, s);
+    } else {
+        launch_tiles<128, 128, 2, 2, 4, F16>(a, s);
     }
-    if (a.T <= 16) f16 ? go(k_int8_skinny<true, 1>, 1) : go(k_int8_skinny<false, 1>, 1);
-    else f16 ? go(k_int8_skinny<true, 4>, 4) : go(k_int8_skinny<false, 4>, 4);
     return hipGetLastError();
+}
+
+hipError_t launch_int8(const Int8Args& a, void*, hipStream_t s, bool f16) {
+    return f16 ? launch_int8_of<true>(a, s) : launch_int8_of<false>(a, s);
 }
 
 }  // namespace ql
