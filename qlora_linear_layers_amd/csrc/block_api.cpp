@@ -83,8 +83,8 @@ int int8_impl(const int8_t* x_codes, const float* x_scale, int64_t T, int64_t K,
     if (need && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
     const ql::Int8Args a{x_codes, x_scale, w_codes, w_scale, y,
                          ql::Epilogue{e->act, e->bias, e->mul, e->residual, nullptr, nullptr, nullptr}, T, N,
-                         (int)ql::rows8_pitch(K)};
-    return dev(ql::launch_int8(a, workspace, static_cast<hipStream_t>(stream), f16));
+                         (int)ql::rows8_pitch(K), 1, nullptr};
+    return dev(ql::launch_int8(a, K, workspace, static_cast<hipStream_t>(stream), f16));
 }
 
 }  // namespace

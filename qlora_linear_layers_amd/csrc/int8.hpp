@@ -19,6 +19,8 @@ struct Int8Args {
     Epilogue ep;              // z, zc and zs unused
     int64_t T, N;
     int P;                    // pitch of a row: K rounded up to 128, zeros past K
+    int splits;               // of the reduction, and their int32 sums [splits][T][N rounded up to 8]
+    int* part;
 };
 
 // Z = sum dx dw.  The smaller scale first: sum * min stays finite and keeps its
@@ -39,7 +41,14 @@ QL_DEV float act_of(int act, float z) {
     }
 }
 
+// Up to 16 tokens a product runs on the decode kernel (no LDS tiles), and up to 32
+// where its workgroups are one a CU and read little of X: each of them reads all of it.
+// Decode kernel / split 64-token tiles, us: 17 tokens through 4096 -> 4096 7.0 / 9.6, 32
+// tokens 8.1 / 10.0, 17 tokens through 11008 -> 4096 13.2 / 13.9, 32 tokens 16.8 / 14.5, 17
+// tokens through 4096 -> 11008 16.6 / 13.4; 16 tokens 13.2 / 13.4.
+constexpr int64_t kInt8SkinnyT = 32, kInt8SkinnyTK = 196608;
+
 size_t int8_workspace(int64_t T, int64_t K, int64_t N);
-hipError_t launch_int8(const Int8Args& a, void* ws, hipStream_t s, bool f16);
+hipError_t launch_int8(Int8Args a, int64_t K, void* ws, hipStream_t s, bool f16);
 
 }  // namespace ql
