@@ -896,49 +896,79 @@ def qlora_linear_act_bwd(dy, qw, lora_a=None, lora_b=None, scaling=1.0, act="non
 
 # ------------------------------------------------------------------ norm, rows in 8 bits, 8-bit integer product
 
-def _one_device(tensors):
-    """Every tensor (None apart) must be on the current device, whose stream the work goes to.
-    Checked after _dev, so all are GPU tensors."""
-    here = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+def _on(t, dtype, name, here):
+    """A given tensor must be dense, of its type and on the current device `here`, whose stream the
+    work goes to."""
+    if t is None or (t.dtype is dtype and t.is_contiguous() and t.get_device() == here):
+        return
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
+def _here():
+    return torch._C._cuda_getDevice()
 
 
 def _matrix(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
-    if t.numel() == 0:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}: rows and columns must be at least 1")
-    return t.shape
+    """(rows, columns) of a matrix with at least one of each."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
+    if shape[0] < 1 or shape[1] < 1:
+        raise ValueError(f"{name} has shape {tuple(shape)}: rows and columns must be at least 1")
+    return shape
 
 
 class Rows8:
     """A matrix in 8 bits with one scale per row (device tensors): `codes` int8 [R, P], rows padded by
-    zeros to the pitch P (rows8_pitch), and `scale` float32 [R]; `shape` is the matrix's (R, K)."""
-    __slots__ = ("codes", "scale", "shape")
+    zeros to the pitch P (rows8_pitch), and `scale` float32 [R]; `shape` is the matrix's (R, K).  One
+    made by rows8_empty holds both in a single allocation, and the two tensors are views made when
+    asked for."""
+    __slots__ = ("shape", "_codes", "_scale", "_buf")
 
     def __init__(self, codes, scale, shape):
-        self.codes, self.scale, self.shape = codes, scale, (int(shape[0]), int(shape[1]))
+        self.shape = (int(shape[0]), int(shape[1]))
+        self._codes, self._scale, self._buf = codes, scale, None
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            R, P = self.shape[0], rows8_pitch(self.shape[1])
+            self._codes = self._buf[:R * P].view(R, P)
+        return self._codes
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            self._scale = self._buf[-4 * self.shape[0]:].view(torch.float32)
+        return self._scale
 
     @property
     def device(self):
-        return self.codes.device
+        return (self._codes if self._buf is None else self._buf).device
 
     def nbytes(self):
-        return self.codes.numel() + 4 * self.scale.numel()
+        return self.shape[0] * (rows8_pitch(self.shape[1]) + 4)
 
     def check(self, name):
-        """The tensors must hold exactly what the shape needs: the C ABI trusts the sizes."""
+        """The tensors must hold exactly what the shape needs (a rows8_empty's do): the C ABI trusts
+        the sizes."""
         R, K = self.shape
         if R < 1 or K < 1:
             raise ValueError(f"{name} has shape {self.shape}: rows and columns must be at least 1")
-        _shape(self.codes, (R, rows8_pitch(K)), name + " codes")
-        _shape(self.scale, (R,), name + " scale")
+        if self._buf is None:
+            _shape(self._codes, (R, rows8_pitch(K)), name + " codes")
+            _shape(self._scale, (R,), name + " scale")
 
-    def dev(self, name):
-        _dev(self.codes, torch.int8, name + " codes")
-        _dev(self.scale, torch.float32, name + " scale")
+    def pointers(self, name, here):
+        """(codes, scale) addresses of checked rows on the current device."""
+        if self._buf is not None:
+            _on(self._buf, torch.int8, name + " codes", here)
+            p = self._buf.data_ptr()
+            return p, p + self.shape[0] * rows8_pitch(self.shape[1])
+        _on(self._codes, torch.int8, name + " codes", here)
+        _on(self._scale, torch.float32, name + " scale", here)
+        return self._codes.data_ptr(), self._scale.data_ptr()
 
 
 def rows8_pitch(K):
@@ -948,9 +978,10 @@ def rows8_pitch(K):
 
 def rows8_empty(shape, device="cuda"):
     """A Rows8 of uninitialised storage for a matrix of `shape` (R, K)."""
-    R, K = shape
-    return Rows8(torch.empty((R, rows8_pitch(K)), dtype=torch.int8, device=device),
-                 torch.empty(R, dtype=torch.float32, device=device), (R, K))
+    r8 = Rows8(None, None, shape)
+    R, K = r8.shape
+    r8._buf = torch.empty(R * (rows8_pitch(K) + 4), dtype=torch.int8, device=device)     # codes, then scales
+    return r8
 
 
 def rows8_quantize(x, out=None):
@@ -961,12 +992,12 @@ def rows8_quantize(x, out=None):
     if out is not None:
         out.check("out")
         _shape(x, out.shape, "x")
-        out.dev("out")
-    _dev(x, x.dtype, "x")
+    here = _here()
+    _on(x, x.dtype, "x", here)
     if out is None:
         out = rows8_empty((R, K), x.device)
-    _one_device((x, out.codes, out.scale))
-    _check(fn, getattr(lib(), fn)(x.data_ptr(), R, K, out.codes.data_ptr(), out.scale.data_ptr(), _stream()))
+    codes, scale = out.pointers("out", here)
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), R, K, codes, scale, _stream()))
     return out
 
 
@@ -974,25 +1005,28 @@ def rows8_dequantize(r8, dtype=torch.bfloat16, out=None):
     """Rows8 -> the 16-bit values [R, K] it stands for, in `dtype` (or in the dtype of `out`)."""
     r8.check("rows")
     _shape(out, r8.shape, "out")
-    r8.dev("rows")
+    here = _here()
+    codes, scale = r8.pointers("rows", here)
     if out is None:
         out = torch.empty(r8.shape, dtype=dtype, device=r8.device)
+    else:
+        _on(out, out.dtype, "out", here)
     fn = "rows8_dequantize" + _ct(out, "out")
-    _dev(out, out.dtype, "out")
-    _one_device((r8.codes, r8.scale, out))
     R, K = r8.shape
-    _check(fn, getattr(lib(), fn)(r8.codes.data_ptr(), r8.scale.data_ptr(), R, K, out.data_ptr(), _stream()))
+    _check(fn, getattr(lib(), fn)(codes, scale, R, K, out.data_ptr(), _stream()))
     return out
 
 
-def _norm_weight(weight, D, dtype):
+def _norm_weight(weight, D, dtype, here):
     """weight_f32 of a norm's weight [D] in the compute type or float32 (or None)."""
     if weight is None:
         return 0
     _shape(weight, (D,), "weight")
-    if weight.dtype not in (dtype, torch.float32):
-        raise TypeError(f"weight must be {dtype} or torch.float32, got {weight.dtype}")
-    return int(weight.dtype == torch.float32)
+    wt = weight.dtype
+    if wt is not dtype and wt is not torch.float32:
+        raise TypeError(f"weight must be {dtype} or torch.float32, got {wt}")
+    _on(weight, wt, "weight", here)
+    return int(wt is torch.float32)
 
 
 def rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, quantize=False, keep_h=True, h=None, out=None):
@@ -1002,8 +1036,7 @@ def rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, quantize=False, keep_h=
     `out` are written into if given; `h` may be the tensor of x or of residual."""
     fn = "rmsnorm_fwd" + _ct(x, "x")
     T, D = _matrix(x, "x")
-    dt = x.dtype
-    w32 = _norm_weight(weight, D, dt)
+    dt, here = x.dtype, _here()
     _shape(residual, (T, D), "residual")
     if h is not None and (residual is None or not keep_h):
         raise ValueError("h is given but there is no sum to keep")
@@ -1015,23 +1048,25 @@ def rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, quantize=False, keep_h=
             out.check("out")
         if tuple(out.shape) != (T, D):
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, D)}")
-    _dev(x, dt, "x")
-    _dev(residual, dt, "residual")
-    _dev(h, dt, "h")
-    if weight is not None:
-        _dev(weight, weight.dtype, "weight")
-    if out is None:
-        out = rows8_empty((T, D), x.device) if quantize else torch.empty((T, D), dtype=dt, device=x.device)
-    elif quantize:
-        out.dev("out")
-    else:
-        _dev(out, dt, "out")
+    w32 = _norm_weight(weight, D, dt, here)
+    _on(x, dt, "x", here)
+    _on(residual, dt, "residual", here)
+    _on(h, dt, "h", here)
     if residual is not None and keep_h and h is None:
-        h = torch.empty((T, D), dtype=dt, device=x.device)
-    y, yc, ys = (None, out.codes, out.scale) if quantize else (out, None, None)
-    _one_device((x, residual, weight, h, y, yc, ys))
-    _check(fn, getattr(lib(), fn)(x.data_ptr(), _ptr(residual), T, D, _ptr(weight), w32, float(eps), _ptr(h), _ptr(y),
-                                  _ptr(yc), _ptr(ys), _stream()))
+        h = torch.empty_like(x)
+    y = yc = ys = None
+    if quantize:
+        if out is None:
+            out = rows8_empty((T, D), x.device)
+        yc, ys = out.pointers("out", here)
+    else:
+        if out is None:
+            out = torch.empty_like(x)
+        else:
+            _on(out, dt, "out", here)
+        y = out.data_ptr()
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), _ptr(residual), T, D, _ptr(weight), w32, float(eps), _ptr(h), y, yc, ys,
+                                  _stream()))
     return out if h is None else (out, h)
 
 
@@ -1054,27 +1089,28 @@ def rmsnorm_bwd(dy, h, weight=None, eps=1e-6, dx_add=None, weight_grad=True, wor
     weight_grad."""
     fn = "rmsnorm_bwd" + _ct(dy, "dy")
     T, D = _matrix(dy, "dy")
-    dt = dy.dtype
+    dt, here = dy.dtype, _here()
     _shape(h, (T, D), "h")
-    w32 = _norm_weight(weight, D, dt)
     weight_grad = weight_grad and weight is not None
     _shape(dx_add, (T, D), "dx_add")
     _shape(dx, (T, D), "dx")
     _grad_out(d_weight, (D,), weight_grad, "d_weight")
-    for t, name in ((dy, "dy"), (h, "h"), (dx_add, "dx_add"), (dx, "dx")):
-        _dev(t, dt, name)
-    if weight is not None:
-        _dev(weight, weight.dtype, "weight")
-        _dev(d_weight, weight.dtype, "d_weight")
-    _dev_workspace(workspace)
+    w32 = _norm_weight(weight, D, dt, here)
+    _on(dy, dt, "dy", here)
+    _on(h, dt, "h", here)
+    _on(dx_add, dt, "dx_add", here)
+    _on(dx, dt, "dx", here)
+    if workspace is not None:
+        _on(workspace, workspace.dtype, "workspace", here)
     if dx is None:
-        dx = torch.empty((T, D), dtype=dt, device=dy.device)
+        dx = torch.empty_like(dy)
     if weight_grad:
+        _on(d_weight, weight.dtype, "d_weight", here)
         if d_weight is None:
-            d_weight = torch.empty((D,), dtype=weight.dtype, device=dy.device)
+            d_weight = torch.empty_like(weight)
         if workspace is None:
-            workspace = torch.empty(max(rmsnorm_workspace_bytes_bwd(T, D), 256), dtype=torch.uint8, device=dy.device)
-    _one_device((dy, h, weight, dx_add, dx, d_weight, workspace))
+            workspace = torch.empty(max(lib().rmsnorm_workspace_bytes_bwd(T, D), 256), dtype=torch.uint8,
+                                    device=dy.device)
     _check(fn, getattr(lib(), fn)(dy.data_ptr(), h.data_ptr(), T, D, _ptr(weight), w32, float(eps), _ptr(dx_add),
                                   dx.data_ptr(), _ptr(d_weight), _ptr(workspace),
                                   0 if workspace is None else workspace.numel(), _stream()))
@@ -1104,24 +1140,28 @@ def int8_linear_fwd(x8, w8, dtype=torch.bfloat16, bias=None, act="none", mul=Non
     dt = dtype if out is None else out.dtype
     if dt not in _HALF:
         raise TypeError(f"out must be bfloat16 or float16, got {dt}")
-    x8.dev("x")
-    w8.dev("w")
-    for t, name in ((bias, "bias"), (mul, "mul"), (residual, "residual"), (out, "out")):
-        _dev(t, dt, name)
-    _dev_workspace(workspace)
+    here = _here()
+    xc, xs = x8.pointers("x", here)
+    wc, ws = w8.pointers("w", here)
+    _on(bias, dt, "bias", here)
+    _on(mul, dt, "mul", here)
+    _on(residual, dt, "residual", here)
+    _on(out, dt, "out", here)
     if out is None:
-        out = torch.empty((T, N), dtype=dt, device=x8.device)
+        like = mul if residual is None else residual
+        out = torch.empty((T, N), dtype=dt, device=x8.device) if like is None else torch.empty_like(like)
     L = lib()
     if workspace is None:
         n = L.int8_linear_workspace_bytes(T, K, N)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=x8.device)
-    _one_device((x8.codes, x8.scale, w8.codes, w8.scale, bias, mul, residual, out, workspace))
+    else:
+        _on(workspace, workspace.dtype, "workspace", here)
     ep = Epilogue(code, _ptr(bias), _ptr(mul), _ptr(residual), None, None, None)
-    fn = "int8_linear_fwd_f16" if dt == torch.float16 else "int8_linear_fwd"
+    fn = "int8_linear_fwd_f16" if dt is torch.float16 else "int8_linear_fwd"
     _check(fn, getattr(L, fn)(
-        x8.codes.data_ptr(), x8.scale.data_ptr(), T, K, N, w8.codes.data_ptr(), w8.scale.data_ptr(), ctypes.byref(ep),
-        out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream()))
+        xc, xs, T, K, N, wc, ws, ctypes.byref(ep), out.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _stream()))
     return out
 
 
