@@ -135,7 +135,7 @@ int rmsnorm_bwd_f16(const uint16_t* dy, const uint16_t* h, int64_t T, int64_t D,
 
 size_t rmsnorm_workspace_bytes_bwd(int64_t T, int64_t D) {
     if (check_rows(T, D, QLORA_NORM_MAX) != QLORA_OK) return 0;
-    return ql::align256((size_t)ql::rmsnorm_bwd_teams(T, D) * D * 4);
+    return ql::align256((size_t)ql::rmsnorm_bwd_partials(T, D) * D * 4);
 }
 
 int int8_linear_fwd(const int8_t* x_codes, const float* x_scale, int64_t T, int64_t K, int64_t N,

@@ -5,6 +5,8 @@
 // (d r / d h_j = -r^3 h_j / D, so the norm's slope takes from g its part along
 // n).  Both are bound by HBM: a row stays in its team's registers (rows.hpp),
 // every input is read once and every output written once.
+#include <algorithm>
+
 #include "rows.hpp"
 
 namespace ql {
@@ -162,46 +164,82 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
     }
 }
 
-// dx of a row per team and step, the teams striding over the rows.  A lane holds
-// the same columns of every row, so its share of dw stays in registers and one
-// fp32 partial row per team is written at the end (DW).
+// dx of a row per team and step, the teams striding over the rows.  A lane holds the
+// same columns of every row, so its share of dw stays in registers, and one fp32
+// partial row per workgroup is written at the end (DW).  Rows up to 8192 values are
+// held in registers, the next row's loads issued before this row's sums (kHold); longer
+// ones are read again after the sums, from the caches.
+//
+// 4096 x 8192 with dx_add and fp32 weights, 268 MB: 52 us and 3.5 us for the sum of
+// the partials.  One workgroup a CU (256): with two 61.9 us in all, against 55.7, with
+// three 68.7 (more partials, and the held rows leave no registers for a second one).
 template <bool F16, bool DW, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, int64_t teams) {
     __shared__ float slots[2][32];
     constexpr int kTeams = team_threads(LANES) / LANES;
+    constexpr bool kHold = LANES < 1024;
     const int lane = (int)threadIdx.x & (LANES - 1), D = a.D;
     const int64_t team = (int64_t)blockIdx.x * kTeams + threadIdx.x / LANES;
     const bool wide = a.w32 || !a.w;
-    WChunk w[CH];
+    constexpr int kRegs = kHold ? CH : 1;
+    WChunk w[kRegs];
+    u32x4_t hn[kRegs], dyn[kRegs], an[kRegs];
     float dw[CH][8];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        w[j] = weight_load<F16>(a.w, a.w32, lane + j * LANES, D);
+        if constexpr (kHold) w[j] = weight_load<F16>(a.w, a.w32, lane + j * LANES, D);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
     }
     const float invD = 1.0f / (float)D;
+    const auto load = [&](int64_t row) {
+        const int64_t at = row * D;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) hn[j] = row_load(a.h + at, lane + j * LANES, D);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) dyn[j] = row_load(a.dy + at, lane + j * LANES, D);
+        if (a.add) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) an[j] = row_load(a.add + at, lane + j * LANES, D);
+        }
+    };
+    if constexpr (kHold)
+        if (team < a.T) load(team);
     int par = 0;
 #pragma unroll 1
     for (int64_t row = team; row < a.T; row += teams) {
         const int64_t at = row * D;
-        u32x4_t hq[CH], dyq[CH], aq[CH];
+        u32x4_t hq[kRegs], dyq[kRegs], aq[kRegs];
+        if constexpr (kHold) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) hq[j] = row_load(a.h + at, lane + j * LANES, D);
-#pragma unroll
-        for (int j = 0; j < CH; ++j) dyq[j] = row_load(a.dy + at, lane + j * LANES, D);
-        if (a.add) {
-#pragma unroll
-            for (int j = 0; j < CH; ++j) aq[j] = row_load(a.add + at, lane + j * LANES, D);
+            for (int j = 0; j < CH; ++j) {
+                hq[j] = hn[j];
+                dyq[j] = dyn[j];
+                aq[j] = an[j];
+            }
+            if (row + teams < a.T) load(row + teams);
         }
+        // chunk j: h, dy and the weights in fp32
+        const auto chunk = [&](int j, float (&h)[8], float (&dy)[8], float (&g)[8]) {
+            const int c = lane + j * LANES;
+            if constexpr (kHold) {
+                unpack8<F16>(hq[j], h);
+                unpack8<F16>(dyq[j], dy);
+                weight_values<F16>(w[j], wide, g);
+            } else {
+                const u32x4_t hc = row_load(a.h + at, c, D), dyc = row_load(a.dy + at, c, D);
+                const WChunk wc = weight_load<F16>(a.w, a.w32, c, D);
+                unpack8<F16>(hc, h);
+                unpack8<F16>(dyc, dy);
+                weight_values<F16>(wc, wide, g);
+            }
+        };
         const auto sums = [&](float pre, float& ss, float& gh) {
             ss = gh = 0.0f;
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 float h[8], dy[8], g[8];
-                unpack8<F16>(hq[j], h);
-                unpack8<F16>(dyq[j], dy);
-                weight_values<F16>(w[j], wide, g);
+                chunk(j, h, dy, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float u = h[e] * pre;
@@ -224,10 +262,17 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
         const float m = gh * r * invD;                  // mean(g n)
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
+            // the packed values are what stays in registers over the sums, not their fp32 forms
+            if constexpr (kHold) asm("" : "+v"(hq[j]), "+v"(dyq[j]));
+            else asm volatile("" ::: "memory");
+            const int c = lane + j * LANES;
             float h[8], dy[8], g[8];
-            unpack8<F16>(hq[j], h);
-            unpack8<F16>(dyq[j], dy);
-            weight_values<F16>(w[j], wide, g);
+            chunk(j, h, dy, g);
+            u32x4_t add = {0, 0, 0, 0};
+            if (a.add) {
+                if constexpr (kHold) add = aq[j];
+                else add = row_load(a.add + at, c, D);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float n = h[e] * pre * r;
@@ -235,21 +280,36 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
                 h[e] = (dy[e] * g[e] - n * m) * r * pre;
             }
             if (a.add) {
-                unpack8<F16>(aq[j], dy);
+                unpack8<F16>(add, dy);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) h[e] += dy[e];
             }
-            row_store(a.dx + at, lane + j * LANES, D, pack8<F16>(h));
+            row_store(a.dx + at, c, D, pack8<F16>(h));
         }
     }
     if constexpr (DW) {
-        if (team < teams) {
+        float* const part = a.part + (int64_t)blockIdx.x * D;
+        if constexpr (kTeams > 1) {
+            // the workgroup's teams are added in team order
+            __shared__ float all[kTeams][LANES * CH * 8];
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) all[threadIdx.x / LANES][(lane + j * LANES) * 8 + e] = dw[j][e];
+            __syncthreads();
+            for (int c = (int)threadIdx.x; c < D; c += team_threads(LANES)) {
+                float v = all[0][c];
+#pragma unroll
+                for (int q = 1; q < kTeams; ++q) v += all[q][c];
+                part[c] = v;
+            }
+        } else {
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 const int e0 = (lane + j * LANES) * 8;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (e0 + e < D) a.part[team * D + e0 + e] = dw[j][e];
+                    if (e0 + e < D) part[e0 + e] = dw[j][e];
             }
         }
     }
@@ -258,14 +318,14 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
 // dw: 64 columns per workgroup, 16 waves that each add every sixteenth partial;
 // their sums are added in wave order.
 template <bool F16>
-__global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float* __restrict__ part, int64_t teams, int D, int w32,
+__global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float* __restrict__ part, int64_t groups, int D, int w32,
                                                      void* __restrict__ dw) {
     __shared__ float sum[16][64];
     const int c = (int)blockIdx.x * 64 + ((int)threadIdx.x & 63), wv = (int)threadIdx.x >> 6;
     float v = 0.0f;
     if (c < D) {
 #pragma unroll 8
-        for (int64_t q = wv; q < teams; q += 16) v += part[q * D + c];
+        for (int64_t q = wv; q < groups; q += 16) v += part[q * D + c];
     }
     sum[wv][threadIdx.x & 63] = v;
     __syncthreads();
@@ -281,8 +341,9 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_dw(const float* __restrict__ p
 
 namespace {
 
-// Team of a forward row: one wave up to 2048 values, 256 threads up to 8192, else
-// 1024.
+// Team of a row: one wave up to 2048 values, 256 threads up to 6144, 512 up to 8192,
+// else 1024 (2048 x 8192: 256 threads 28.4 us, 512 26.0, 1024 26.2 to 8 bits and 28.7 to
+// 16).
 template <class Go>
 void for_norm_team(int64_t D, Go go) {
     const int64_t c = ceil_div(D, 8);
@@ -290,12 +351,16 @@ void for_norm_team(int64_t D, Go go) {
     else if (c <= 128) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
     else if (c <= 256) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
     else if (c <= 512) go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    else if (c <= 1024) go(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    else if (c <= 768) go(std::integral_constant<int, 256>{}, std::integral_constant<int, 3>{});
+    else if (c <= 1024) go(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
     else if (c <= 2048) go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
     else go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
-int bwd_lanes(int64_t D) { return D <= 2048 ? 64 : D <= 8192 ? 256 : 1024; }
+// Workgroups of the backward (one a CU) and its teams
+constexpr int64_t kBwdGroups = 256;
+int64_t bwd_per(int64_t D) { return D <= 2048 ? 4 : 1; }
+int64_t bwd_groups(int64_t T, int64_t D) { return std::min(kBwdGroups, ceil_div(T, bwd_per(D))); }
 
 }  // namespace
 
@@ -314,16 +379,13 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s, bool f16) {
     return hipGetLastError();
 }
 
-int64_t rmsnorm_bwd_teams(int64_t T, int64_t D) {
-    const int64_t most = bwd_lanes(D) == 64 ? 1024 : bwd_lanes(D) == 256 ? 512 : 256;
-    return T < most ? T : most;
-}
+int64_t rmsnorm_bwd_partials(int64_t T, int64_t D) { return bwd_groups(T, D); }
 
 hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16) {
-    const int64_t teams = rmsnorm_bwd_teams(a.T, a.D);
+    const int64_t groups = bwd_groups(a.T, a.D), teams = groups * bwd_per(a.D);
     for_norm_team(a.D, [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
-        const dim3 g((unsigned)ceil_div(teams, team_threads(L) / L)), b(team_threads(L));
+        const dim3 g((unsigned)groups), b(team_threads(L));
         if (a.dw) {
             if (f16) hipLaunchKernelGGL((k_rmsnorm_bwd<true, true, L, C>), g, b, 0, s, a, teams);
             else hipLaunchKernelGGL((k_rmsnorm_bwd<false, true, L, C>), g, b, 0, s, a, teams);
@@ -334,8 +396,8 @@ hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16) {
     });
     if (a.dw) {
         const dim3 g((unsigned)ceil_div(a.D, 64));
-        if (f16) hipLaunchKernelGGL(k_rmsnorm_dw<true>, g, dim3(1024), 0, s, a.part, teams, a.D, a.w32, a.dw);
-        else hipLaunchKernelGGL(k_rmsnorm_dw<false>, g, dim3(1024), 0, s, a.part, teams, a.D, a.w32, a.dw);
+        if (f16) hipLaunchKernelGGL(k_rmsnorm_dw<true>, g, dim3(1024), 0, s, a.part, groups, a.D, a.w32, a.dw);
+        else hipLaunchKernelGGL(k_rmsnorm_dw<false>, g, dim3(1024), 0, s, a.part, groups, a.D, a.w32, a.dw);
     }
     return hipGetLastError();
 }
