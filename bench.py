@@ -774,6 +774,41 @@ def measure_mlp(api, torch, synth, reps=10):
     return out, saved.nbytes()
 
 
+def measure_block(api, torch, synth, reps=10):
+    """The pre-norm block of the LLaMA-7B shapes (mlp.py: norm, gated feed-forward, residual stream), r = 64: a
+    training forward and backward at T = 2048, the inference forward on 4-bit weights and on the merged block's 8-bit
+    integers at several token counts.  HIP events over `reps` passes after two warm-up passes.  {name: microseconds}."""
+    from qlora_linear_layers_amd.mlp import AdaptedLinear, GatedMlp, Int8Mlp, NormMlp
+    g = torch.Generator(device="cuda").manual_seed(1)
+    normal = lambda *sh, std=1.0: torch.randn(sh, generator=g, device="cuda").mul_(std).to(torch.bfloat16)
+    by = {l.name: l for l in synth.LLAMA7B}
+    lin = {n: AdaptedLinear(api.nf4_quantize_dq(normal(by[n].N, by[n].K, std=0.02)), normal(by[n].K, 64, std=0.01),
+                            normal(64, by[n].N, std=0.01), 0.25) for n in ("gate", "up", "down")}
+    D = by["gate"].K
+    block = NormMlp(GatedMlp(lin["gate"], lin["up"], lin["down"]), 1.0 + normal(D, std=0.1).float())
+    served = Int8Mlp.from_block(block)
+
+    def us(fn):
+        for _ in range(2):
+            fn()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(reps):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        return 1e3 * a.elapsed_time(b) / reps
+    T = 2048
+    x, res, dy = normal(T, D), normal(T, D), normal(T, D)
+    _, saved = block.forward_train(x, res)
+    out = {"forward_train_T2048_us": us(lambda: block.forward_train(x, res)),
+           "backward_T2048_us": us(lambda: block.backward(dy, saved))}
+    for t in (1, 8, 64, 512, 2048):
+        out[f"forward_4bit_T{t}_us"] = us(lambda: block.forward(x[:t], res[:t]))
+        out[f"forward_int8_T{t}_us"] = us(lambda: served.forward(x[:t], res[:t]))
+    return out
+
+
 def only_component(name, api, torch, synth, calib, args):
     """One component alone (for kernel traces and counter runs)."""
     layers7, r, s = synth.TRAIN_7B["layers"], synth.TRAIN_7B["r"], synth.TRAIN_7B["scaling"]
@@ -817,6 +852,8 @@ def only_component(name, api, torch, synth, calib, args):
     if name == "mlp_7b":
         res, kept = measure_mlp(api, torch, synth)
         return {**{k: round(v, 2) for k, v in res.items()}, "checkpoint_bytes_T2048": kept}
+    if name == "block_7b":
+        return {k: round(v, 2) for k, v in measure_block(api, torch, synth).items()}
     if name == "calibration":
         return {k: round(v / 1e9, 1) for k, v in measure_calibration(torch, calib).items()}
     secs, moved, packed, params = measure_stream_70b(torch, synth)
@@ -834,7 +871,7 @@ def main():
                     help="only the headline step and the roofline kernel (for a kernel trace of the step alone)")
     ap.add_argument("--only", choices=("decode", "decode_single", "decode_all7", "decode_valu", "decode_all7_valu",
                                        "decode_mfma", "decode_all7_mfma", "single_layer", "train_7b", "train_7b_fused", "forward_midt", "train_midt",
-                                       "merge", "mlp_7b", "calibration", "stream_70b"),
+                                       "merge", "mlp_7b", "block_7b", "calibration", "stream_70b"),
                     help="run one component alone (no step, roofline loop or CPU baseline), e.g. for a kernel trace")
     ap.add_argument("--roofline-only", action="store_true",
                     help="only the calibration copy and the k_fwd launches at the 65B shapes (for counter runs)")

@@ -18,10 +18,11 @@ extern "C" {
 #endif
 
 /* Longest row of rows8_quantize and of the 8-bit product (whose int32 sums then
- * stay below 2^31), longest row of the norm, and most rows. */
+ * stay below 2^31), longest row of the norm, and most rows (a grid of one
+ * 1024-thread workgroup a row stays below 2^32 threads). */
 #define QLORA_ROWS8_MAX 65536
 #define QLORA_NORM_MAX 32768
-#define QLORA_ROWS_MAX 16777216
+#define QLORA_ROWS_MAX 2097152
 /* Bytes from one row of codes to the next: K rounded up to a multiple of 128. */
 #define QLORA_ROWS8_PITCH(K) (((int64_t)(K) + 127) / 128 * 128)
 
@@ -106,7 +107,7 @@ size_t rmsnorm_workspace_bytes_bwd(int64_t T, int64_t D);
  *   its row of Y (its column, for a channel of W) NaN.
  *   x_codes [T, QLORA_ROWS8_PITCH(K)], x_scale [T]; w_codes [N, same pitch],
  *   w_scale [N]: as rows8_quantize or rmsnorm_fwd writes them (zeros past K).
- *   T 1 .. 2^22, N 1 .. 2^20, K 1 .. QLORA_ROWS8_MAX, T N and T K at most 2^30.
+ *   T 1 .. QLORA_ROWS_MAX, N 1 .. 2^20, K 1 .. QLORA_ROWS8_MAX, T N and T K at most 2^30.
  *   epilogue: bias [N], mul and residual [T, N] of Y's type or NULL, act; its
  *   z, z_codes and z_scale must be NULL.  y [T, N], written; may be the buffer of
  *   mul or of residual; no other overlap.

@@ -66,7 +66,7 @@ int norm_bwd_impl(const uint16_t* dy, const uint16_t* h, int64_t T, int64_t D, c
 }
 
 int check_int8_shape(int64_t T, int64_t K, int64_t N) {
-    if (T < 1 || K < 1 || N < 1 || T > (int64_t(1) << 22) || N > (int64_t(1) << 20) || K > QLORA_ROWS8_MAX)
+    if (T < 1 || K < 1 || N < 1 || T > QLORA_ROWS_MAX || N > (int64_t(1) << 20) || K > QLORA_ROWS8_MAX)
         return QLORA_ERR_SHAPE;
     return T * K > (int64_t(1) << 30) || T * N > (int64_t(1) << 30) ? QLORA_ERR_SHAPE : QLORA_OK;
 }

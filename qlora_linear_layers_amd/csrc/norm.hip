@@ -55,12 +55,14 @@ QL_DEV void weight_values(const WChunk& k, bool wide, float (&v)[8]) {
     }
 }
 
-// Rows whose squares leave fp32 (rms above 2^64 or so) are summed scaled by this
-// power of two, which eps and the precision do not notice there; the sum of an
-// inf stays inf (r = 0), of a NaN NaN.
+// Rows whose squares leave fp32 (rms above 2^64 / sqrt D) are summed scaled by this
+// power of two (exact); the sum of an inf stays inf (r = 0), of a NaN NaN.
 constexpr float kHuge = 0x1p-72f;
 
-QL_DEV float inv_rms(float ss, int D, float eps) { return __builtin_amdgcn_rsqf(ss / (float)D + eps); }
+// 1 / sqrt of the mean square of the row times `pre` (1 or kHuge), eps scaled with it
+QL_DEV float inv_rms(float ss, int D, float eps, float pre) {
+    return __builtin_amdgcn_rsqf(ss / (float)D + (pre == 1.0f ? eps : eps * (kHuge * kHuge)));
+}
 
 }  // namespace
 
@@ -117,7 +119,7 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
         if constexpr (LANES > 64) __syncthreads();      // slots[0] is read
         ss = team_sum<LANES>(squares(pre), slots[0]);
     }
-    const float r = inv_rms(ss, D, pre == 1.0f ? a.eps : 0.0f);
+    const float r = inv_rms(ss, D, a.eps, pre);
     const bool wide = a.w32 || !a.w;
     const auto normed = [&](int j, float (&y)[8]) {
         float g[8];
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
             team_sum2<LANES>(ss, gh, slots[par]);
         }
         par ^= 1;
-        const float r = inv_rms(ss, D, pre == 1.0f ? a.eps : 0.0f);
+        const float r = inv_rms(ss, D, a.eps, pre);
         const float m = gh * r * invD;                  // mean(g n)
 #pragma unroll
         for (int j = 0; j < CH; ++j) {

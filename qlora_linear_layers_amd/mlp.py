@@ -139,7 +139,7 @@ class NormMlp:
         return y, NormMlpSaved(h, saved)
 
     def backward(self, dy, saved, norm_grad=True):
-        """NormMlpGrads for the upstream gradient dY [T, D]."""
+        """NormMlpGrads for the upstream gradient dY [T, D] (its mlp.dx is the buffer that dx is formed in)."""
         m = self.mlp.backward(dy, saved.mlp)
         g = api.rmsnorm_bwd(m.dx, saved.h, self.norm_weight, self.eps, dx_add=dy, weight_grad=norm_grad, dx=m.dx)
         return NormMlpGrads(g.dx, g.d_weight, m)

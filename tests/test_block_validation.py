@@ -33,7 +33,7 @@ def test_rows8_refusals(L, suffix):
         assert f(None, 4, 64, FAKE, FAKE, None) == NULL
         assert f(FAKE, 4, 64, None, FAKE, None) == NULL
         assert f(FAKE, 4, 64, FAKE, None, None) == NULL
-        for r, k in ((0, 64), (-1, 64), (4, 0), (4, -5), (4, 65537), ((1 << 24) + 1, 64)):
+        for r, k in ((0, 64), (-1, 64), (4, 0), (4, -5), (4, 65537), ((1 << 21) + 1, 64)):
             assert f(FAKE, r, k, FAKE, FAKE, None) == SHAPE, (r, k)
         assert f(MIS, 4, 64, FAKE, FAKE, None) == ALIGN
         assert f(FAKE, 4, 64, MIS, FAKE, None) == ALIGN
@@ -46,7 +46,7 @@ def test_norm_refusals(L, suffix):
         return getattr(L, "rmsnorm_fwd" + suffix)(x, res, T, D, w, w32, eps, h, y, yc, ys, None)
     assert call(x=None) == NULL and call(y=None) == NULL
     assert call(yc=FAKE) == NULL and call(ys=FAKE) == NULL
-    for bad in (dict(T=0), dict(T=-3), dict(T=(1 << 24) + 1), dict(D=0), dict(D=32769)):
+    for bad in (dict(T=0), dict(T=-3), dict(T=(1 << 21) + 1), dict(D=0), dict(D=32769)):
         assert call(**bad) == SHAPE, bad
     for k in ("x", "res", "w", "h", "y"):
         assert call(**{k: MIS}) == ALIGN, k
@@ -87,7 +87,7 @@ def test_product_refusals(L, suffix):
     assert call(ep=False) == NULL and call(ws=MIS) == ALIGN
     for k in ("bias", "mul", "residual"):
         assert call(**{k: MIS}) == ALIGN, k
-    for bad in (dict(T=0), dict(K=0), dict(N=0), dict(K=65537), dict(N=(1 << 20) + 1), dict(T=(1 << 22) + 1),
+    for bad in (dict(T=0), dict(K=0), dict(N=0), dict(K=65537), dict(N=(1 << 20) + 1), dict(T=(1 << 21) + 1),
                 dict(T=1 << 20, K=2048), dict(T=1 << 20, N=2048)):
         assert call(**bad) == SHAPE, bad
         full = {**dict(T=5, K=100, N=70), **bad}

@@ -206,6 +206,10 @@ def test_norm_over_the_types_range(D):
     yn = f64(y)
     assert np.isnan(yn[5, 7]) and (np.delete(yn[5], 7) == 0).all() and np.isnan(yn[6]).all()
     assert np.isnan(f64(y8)[5:7]).all()
+    # an eps as large as such rows' mean square counts there, too
+    e = api.rmsnorm_fwd(x[7:8].contiguous(), w, 3e38)
+    ref = oracle.rmsnorm(f64(x)[7:8], f64(w), 3e38)
+    within(e, ref, norm_bound(ref, dt), "y with a large eps")
     hv, dv = f64(x)[fine], f64(dy)[fine]
     rdx = oracle.rmsnorm_bwd(dv, hv, f64(w), 1e-6)[0]
     within(f64(g.dx)[fine], rdx, bwd_bound(rdx, dv, hv, f64(w), 1e-6, dt), "dx")
