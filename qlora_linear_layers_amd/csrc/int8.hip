@@ -505,50 +505,77 @@ void launch_tiles(const Int8Args& a, hipStream_t s) {
 }
 
 // The sums of all splits, and the epilogue: eight channels of a token per thread, one
-// wave per workgroup, so that few tokens spread over the CUs (64 x 4096 of eight splits,
-// 8 MB: 4.2 us, of 256-thread workgroups with a division for the row 5.4).
-template <bool F16>
+// wave per workgroup, so that few tokens spread over the CUs.  The number of splits is a
+// template argument and the operands of the epilogue come before the sums, so that every
+// load of a thread is in flight at once: 61 x 4097 of five splits (5 MB) 3.3 us, with a
+// loop over the splits and the operands after it 5.1.  Channels behind the last whole
+// eight go one by one.
+template <bool F16, int S>
 __global__ __launch_bounds__(64) void k_int8_fin(Int8Args a) {
     const int N = (int)a.N, NP = (N + 7) & ~7;
     const int n = ((int)blockIdx.x * 64 + (int)threadIdx.x) * 8;
     const int64_t t = blockIdx.y;
     if (n >= N) return;
-    const int64_t at = t * NP + n, step = a.T * NP;
-    i32x4_t lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-#pragma unroll 8
-    for (int q = 0; q < a.splits; ++q) {
-        const i32x4_t* const p = reinterpret_cast<const i32x4_t*>(a.part + at + q * step);
-        lo += p[0];
-        hi += p[1];
-    }
-    const int sum[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    const float xs = a.xs[t];
-    float v[8], w[8];
-    const int c = n / 8;
+    const int64_t step = a.T * NP, o = t * N + n;
+    const i32x4_t* const p = reinterpret_cast<const i32x4_t*>(a.part + t * NP + n);
+    i32x4_t lo[S], hi[S];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = int8_scaled(sum[e], xs, n + e < N ? a.ws[n + e] : 0.0f);
+    for (int q = 0; q < S; ++q) {
+        lo[q] = p[q * step / 4];
+        hi[q] = p[q * step / 4 + 1];
+    }
+    const auto add = [&]() {
+#pragma unroll
+        for (int q = 1; q < S; ++q) {
+            lo[0] += lo[q];
+            hi[0] += hi[q];
+        }
+    };
+    if (n + 8 > N) {
+        add();
+#pragma unroll 1
+        for (int e = 0; n + e < N; ++e) {
+            int v = lo[0][0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) v = e == q ? (q < 4 ? lo[0][q] : hi[0][q - 4]) : v;
+            a.y[o + e] = epi_value<F16>(a, epi_load(a, t, n + e), v);
+        }
+        return;
+    }
+    const float xs = a.xs[t];
+    const u32x4_t w0 = *reinterpret_cast<const u32x4_t*>(a.ws + n), w1 = *reinterpret_cast<const u32x4_t*>(a.ws + n + 4);
+    u32x4_t bias = {0, 0, 0, 0}, mul = bias, res = bias;
+    if (a.ep.bias) bias = *reinterpret_cast<const u32x4_t*>(a.ep.bias + n);
+    if (a.ep.mul) mul = *reinterpret_cast<const u32x4_a2*>(a.ep.mul + o);
+    if (a.ep.res) res = *reinterpret_cast<const u32x4_a2*>(a.ep.res + o);
+    add();
+    float v[8], w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = int8_scaled(e < 4 ? lo[0][e] : hi[0][e - 4], xs, __uint_as_float(e < 4 ? w0[e] : w1[e - 4]));
     if (a.ep.bias) {
-        unpack8<F16>(row_load(a.ep.bias, c, N), w);
+        unpack8<F16>(bias, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += w[e];
     }
     act_values(a.ep.act, v);
     if (a.ep.mul) {
-        unpack8<F16>(row_load(a.ep.mul + t * N, c, N), w);
+        unpack8<F16>(mul, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= w[e];
     }
     if (a.ep.res) {
-        unpack8<F16>(row_load(a.ep.res + t * N, c, N), w);
+        unpack8<F16>(res, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += w[e];
     }
-    row_store(a.y + t * N, c, N, pack8<F16>(v));
+    *reinterpret_cast<u32x4_a2*>(a.y + o) = pack8<F16>(v);
 }
 
 namespace {
 
 // Which kernel takes a product, and the splits of its reduction.
+constexpr int kInt8MaxSplits = 8;
 enum class Int8Route { Skinny, Tile64, Tile128, Tile256 };
 struct Int8Plan {
     Int8Route route;
@@ -573,7 +600,7 @@ struct Int8Plan {
             return (double)ceil_div(tiles * s, 256) * (double)ceil_div(kt, s) * 0.34 +
                    (s > 1 ? 2.5 + 0.4e-6 * (double)(s * T * N * 4) : 0.0);
         };
-        for (int s = 2; s <= 8 && kt / s >= 2 && tiles * s <= 256; ++s)
+        for (int s = 2; s <= kInt8MaxSplits && kt / s >= 2 && tiles * s <= 256; ++s)
             if (cost(s) < cost(splits)) splits = s;
         if (splits == 1) return;
         bytes = align256((size_t)splits * T * ((N + 7) & ~int64_t(7)) * 4);
@@ -599,7 +626,18 @@ static hipError_t launch_int8_of(const Int8Args& a, const Int8Plan& pl, hipStrea
     } else if (pl.splits > 1) {
         if (pl.route == Int8Route::Tile64) part(k_int8_tile<false, kActPart, 128, 64, 2, 2, 4>, 64);
         else part(k_int8_tile<false, kActPart, 128, 128, 2, 2, 4>, 128);
-        hipLaunchKernelGGL(k_int8_fin<F16>, dim3((unsigned)ceil_div(a.N, 512), (unsigned)a.T), dim3(64), 0, s, a);
+        const auto fin = [&](auto kern) {
+            hipLaunchKernelGGL(kern, dim3((unsigned)ceil_div(a.N, 512), (unsigned)a.T), dim3(64), 0, s, a);
+        };
+        switch (pl.splits) {
+            case 2: fin(k_int8_fin<F16, 2>); break;
+            case 3: fin(k_int8_fin<F16, 3>); break;
+            case 4: fin(k_int8_fin<F16, 4>); break;
+            case 5: fin(k_int8_fin<F16, 5>); break;
+            case 6: fin(k_int8_fin<F16, 6>); break;
+            case 7: fin(k_int8_fin<F16, 7>); break;
+            default: fin(k_int8_fin<F16, 8>); break;
+        }
     } else if (pl.route == Int8Route::Tile256) {
         launch_tiles<256, 256, 2, 2, 2, F16>(a, s);
     } else if (pl.route == Int8Route::Tile64) {
