@@ -1037,10 +1037,14 @@ def rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, quantize=False, keep_h=
     fn = "rmsnorm_fwd" + _ct(x, "x")
     T, D = _matrix(x, "x")
     dt, here = x.dtype, _here()
-    _shape(residual, (T, D), "residual")
-    if h is not None and (residual is None or not keep_h):
-        raise ValueError("h is given but there is no sum to keep")
-    _shape(h, (T, D), "h")
+    if residual is not None:
+        _shape(residual, (T, D), "residual")
+        _on(residual, dt, "residual", here)
+    if h is not None:
+        if residual is None or not keep_h:
+            raise ValueError("h is given but there is no sum to keep")
+        _shape(h, (T, D), "h")
+        _on(h, dt, "h", here)
     if out is not None:
         if isinstance(out, Rows8) != bool(quantize):
             raise ValueError("out must be a Rows8 with quantize and a tensor without")
@@ -1050,9 +1054,7 @@ def rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, quantize=False, keep_h=
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(T, D)}")
     w32 = _norm_weight(weight, D, dt, here)
     _on(x, dt, "x", here)
-    _on(residual, dt, "residual", here)
-    _on(h, dt, "h", here)
-    if residual is not None and keep_h and h is None:
+    if h is None and residual is not None and keep_h:
         h = torch.empty_like(x)
     y = yc = ys = None
     if quantize:
@@ -1133,19 +1135,17 @@ def int8_linear_fwd(x8, w8, dtype=torch.bfloat16, bias=None, act="none", mul=Non
     (T, K), N = x8.shape, w8.shape[0]
     if w8.shape[1] != K:
         raise ValueError(f"w has shape {w8.shape}, expected rows of {K}")
-    _shape(bias, (N,), "bias")
-    _shape(mul, (T, N), "mul")
-    _shape(residual, (T, N), "residual")
     _shape(out, (T, N), "out")
     dt = dtype if out is None else out.dtype
     if dt not in _HALF:
         raise TypeError(f"out must be bfloat16 or float16, got {dt}")
     here = _here()
+    for t, shape, name in ((bias, (N,), "bias"), (mul, (T, N), "mul"), (residual, (T, N), "residual")):
+        if t is not None:
+            _shape(t, shape, name)
+            _on(t, dt, name, here)
     xc, xs = x8.pointers("x", here)
     wc, ws = w8.pointers("w", here)
-    _on(bias, dt, "bias", here)
-    _on(mul, dt, "mul", here)
-    _on(residual, dt, "residual", here)
     _on(out, dt, "out", here)
     if out is None:
         like = mul if residual is None else residual
