@@ -594,11 +594,14 @@ struct Int8Plan {
         }
         route = T <= 64 ? Int8Route::Tile64 : Int8Route::Tile128;
         // Splits: rounds of K tiles at 0.34 us, and for the int32 sums, written and read
-        // back, 0.4 us a MB and 2.5 us of a launch (fitted to the times below).
+        // back, 0.4 us a MB and 1.5 us of a launch.  Against 0.25 us a MB and 2 of a launch,
+        // us: 128 tokens through 11008 -> 4096 18.9 / 20.2 (6 / 8 splits), 256 through 4096 ->
+        // 1024 11.7 / 13.2; with 2.5 of a launch 256 through 4096 -> 4096 stay unsplit, 16.8
+        // against 15.3, 300 through 5120 -> 5120 21.7 against 20.0.
         const int64_t tiles = ceil_div(N, 128) * ceil_div(T, T <= 64 ? 64 : 128);
         const auto cost = [&](int64_t s) {
             return (double)ceil_div(tiles * s, 256) * (double)ceil_div(kt, s) * 0.34 +
-                   (s > 1 ? 2.5 + 0.4e-6 * (double)(s * T * N * 4) : 0.0);
+                   (s > 1 ? 1.5 + 0.4e-6 * (double)(s * T * N * 4) : 0.0);
         };
         for (int s = 2; s <= kInt8MaxSplits && kt / s >= 2 && tiles * s <= 256; ++s)
             if (cost(s) < cost(splits)) splits = s;

@@ -43,9 +43,11 @@ QL_DEV float act_of(int act, float z) {
 
 // Up to 16 tokens a product runs on the decode kernel (no LDS tiles), and up to 32
 // where its workgroups are one a CU and read little of X: each of them reads all of it.
-// Decode kernel / split 64-token tiles, us: 17 tokens through 4096 -> 4096 7.0 / 9.6, 32
-// tokens 8.1 / 10.0, 17 tokens through 11008 -> 4096 13.2 / 13.9, 32 tokens 16.8 / 14.5, 17
-// tokens through 4096 -> 11008 16.6 / 13.4; 16 tokens 13.2 / 13.4.
+// Decode kernel / split 64-token tiles, us: 17 tokens through 4096 -> 4096 6.7 / 8.5, 32
+// tokens 7.9 / 9.1, 20 tokens through 8192 -> 4096 11.0 / 11.2, 24 tokens 11.6 / 10.9, 32
+// tokens through 11008 -> 4096 16.8 / 13.4, 17 tokens through 4096 -> 11008 16.6 / 12.3, 16
+// tokens 13.2 / 12.2.  Up to a microsecond is given away for one launch and no workspace,
+// which a call from the host (8 against 14 us of its own) gains back.
 constexpr int64_t kInt8SkinnyT = 32, kInt8SkinnyTK = 196608;
 
 size_t int8_workspace(int64_t T, int64_t K, int64_t N);
