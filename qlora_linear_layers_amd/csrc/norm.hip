@@ -100,8 +100,13 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
         for (int j = 0; j < CH; ++j) w[j] = weight_load<F16>(a.w, a.w32, lane + j * LANES, D);
     }
     if (a.h && ok) {
+        if (a.far) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) row_store(a.h + at, lane + j * LANES, D, h[j]);
+            for (int j = 0; j < CH; ++j) row_store_far(a.h + at, lane + j * LANES, D, h[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) row_store(a.h + at, lane + j * LANES, D, h[j]);
+        }
     }
     const auto squares = [&](float pre) {
         float s = 0.0f;
@@ -178,7 +183,7 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
 // the sum of the partials.  One workgroup a CU (256): with two 61.9 us in all, against
 // 55.7, with three 68.7 (more partials, and the held rows leave no registers for a second
 // one).
-template <bool F16, bool DW, int LANES, int CH>
+template <bool F16, bool DW, bool FAR, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, int64_t teams) {
     __shared__ float slots[2][32];
     constexpr int kTeams = team_threads(LANES) / LANES;
@@ -199,13 +204,14 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
     const float invD = 1.0f / (float)D;
     const auto load = [&](int64_t row) {
         const int64_t at = row * D;
+        const auto get = [&](const uint16_t* p, int c) { return FAR ? row_load_far(p, c, D) : row_load(p, c, D); };
 #pragma unroll
-        for (int j = 0; j < CH; ++j) hn[j] = row_load(a.h + at, lane + j * LANES, D);
+        for (int j = 0; j < CH; ++j) hn[j] = get(a.h + at, lane + j * LANES);
 #pragma unroll
-        for (int j = 0; j < CH; ++j) dyn[j] = row_load(a.dy + at, lane + j * LANES, D);
+        for (int j = 0; j < CH; ++j) dyn[j] = get(a.dy + at, lane + j * LANES);
         if (a.add) {
 #pragma unroll
-            for (int j = 0; j < CH; ++j) an[j] = row_load(a.add + at, lane + j * LANES, D);
+            for (int j = 0; j < CH; ++j) an[j] = get(a.add + at, lane + j * LANES);
         }
     };
     if constexpr (kHold)
@@ -362,6 +368,17 @@ void for_norm_team(int64_t D, Go go) {
     else go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
+// From here on h is stored past the caches (it is read again behind a block's products or
+// in the backward), and from twice as many values on the backward reads its rows, for the
+// last time, that way: what the next kernel needs stays in the 256 MB cache instead.  With
+// a consumer of y (dx) behind each call, us without / with: forward 2048 x 8192 35.4 / 32.0,
+// 4096 x 8192 66.4 / 62.1, backward 4096 x 8192 74.4 / 69.0, 8192 x 8192 154 / 126, 32768 x
+// 1024 70 / 67.  Below, everything fits the cache: forward 2048 x 4096 with h read next 17.2 /
+// 19.0, backward 2048 x 4096 25.0 / 26.5.  (Where h is read at once at 2048 x 8192, 30.8 / 33.4.)
+// Not for rows of odd alignment, whose lines are read twice: backward 777 x 4099 28.4 / 33.3.
+// In the backward a template argument: a branch around the loads cost 57 us against 49.6.
+constexpr int64_t kFarValues = int64_t(1) << 24;
+
 // Workgroups of the backward (one a CU) and its teams
 constexpr int64_t kBwdGroups = 256;
 int64_t bwd_per(int64_t D) { return D <= 2048 ? 4 : 1; }
@@ -369,7 +386,8 @@ int64_t bwd_groups(int64_t T, int64_t D) { return std::min(kBwdGroups, ceil_div(
 
 }  // namespace
 
-hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s, bool f16) {
+hipError_t launch_rmsnorm(NormArgs a, hipStream_t s, bool f16) {
+    a.far = a.T * a.D >= kFarValues;
     for_norm_team(a.D, [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
         const dim3 g((unsigned)ceil_div(a.T, team_threads(L) / L)), b(team_threads(L));
@@ -388,16 +406,17 @@ int64_t rmsnorm_bwd_partials(int64_t T, int64_t D) { return bwd_groups(T, D); }
 
 hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16) {
     const int64_t groups = bwd_groups(a.T, a.D), teams = groups * bwd_per(a.D);
+    const bool far = a.T * a.D >= 2 * kFarValues && a.D % 8 == 0;
     for_norm_team(a.D, [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
         const dim3 g((unsigned)groups), b(team_threads(L));
-        if (a.dw) {
-            if (f16) hipLaunchKernelGGL((k_rmsnorm_bwd<true, true, L, C>), g, b, 0, s, a, teams);
-            else hipLaunchKernelGGL((k_rmsnorm_bwd<false, true, L, C>), g, b, 0, s, a, teams);
-        } else {
-            if (f16) hipLaunchKernelGGL((k_rmsnorm_bwd<true, false, L, C>), g, b, 0, s, a, teams);
-            else hipLaunchKernelGGL((k_rmsnorm_bwd<false, false, L, C>), g, b, 0, s, a, teams);
-        }
+        const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, g, b, 0, s, a, teams); };
+        const auto of = [&](auto f) {
+            constexpr bool F = decltype(f)::value && L < 1024;
+            if (a.dw) f16 ? go(k_rmsnorm_bwd<true, true, F, L, C>) : go(k_rmsnorm_bwd<false, true, F, L, C>);
+            else f16 ? go(k_rmsnorm_bwd<true, false, F, L, C>) : go(k_rmsnorm_bwd<false, false, F, L, C>);
+        };
+        far ? of(std::true_type{}) : of(std::false_type{});
     });
     if (a.dw) {
         const dim3 g((unsigned)ceil_div(a.D, 64));

@@ -47,6 +47,16 @@ QL_DEV void row_store(uint16_t* row, int c, int D, const u32x4_t& v) {
     }
 }
 
+// The same for data that is not needed again soon: the caches let go of it first.
+QL_DEV u32x4_t row_load_far(const uint16_t* row, int c, int D) {
+    if (c * 8 + 8 <= D) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(row + c * 8));
+    return row_load(row, c, D);
+}
+QL_DEV void row_store_far(uint16_t* row, int c, int D, const u32x4_t& v) {
+    if (c * 8 + 8 <= D) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(row + c * 8));
+    else row_store(row, c, D, v);
+}
+
 // ------------------------------------------------------------------ reductions over a team
 
 template <class F>
@@ -162,6 +172,7 @@ struct NormArgs {
     int64_t T;
     int D, w32;
     float eps;
+    bool far;                 // set by the launch: h is written past the caches
 };
 struct NormBwd {
     const uint16_t* dy;
@@ -176,7 +187,7 @@ struct NormBwd {
     float eps;
 };
 
-hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s, bool f16);
+hipError_t launch_rmsnorm(NormArgs a, hipStream_t s, bool f16);
 int64_t rmsnorm_bwd_partials(int64_t T, int64_t D);    // fp32 partial rows of dw
 hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16);
 hipError_t launch_rows8_quantize(const uint16_t* x, int64_t R, int64_t K, int8_t* codes, float* scale, hipStream_t s,

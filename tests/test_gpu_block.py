@@ -255,6 +255,53 @@ def test_norm_backward(T, D, dtype, add, weight):
         assert torch.equal(api.rmsnorm_bwd(dy, h, w, 1e-5, dx_add=t, dx=t).dx, g.dx)
 
 
+# Sizes whose rows pass by the caches (2^24 values in the forward, 2^25 in the backward): rows
+# of one call do not depend on each other, so a few of them alone give the same bits.
+@pytest.mark.parametrize("T,D,dtype", [(2049, 8192, "bf16"), (2050, 8193, "fp16"), (16397, 1024, "bf16"),
+                                       (1025, 16392, "bf16")])
+@pytest.mark.parametrize("quantize", [False, True])
+def test_norm_of_large_batches(T, D, dtype, quantize):
+    say(f"[norm, large] {T} x {D} {dtype} quantize={quantize}")
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    x, res = (torch.randn((T, D), generator=g, device="cuda").to(dt) for _ in range(2))
+    w = torch.randn(D, generator=g, device="cuda").to(dt)
+    h, h_kept = behind(T, D, dt)
+    y, _ = api.rmsnorm_fwd(x, w, 1e-5, residual=res, quantize=quantize, h=h)
+    for lo, hi in ((0, 9), (T // 2, T // 2 + 5), (T - 7, T)):
+        ys, hs = api.rmsnorm_fwd(x[lo:hi].clone(), w, 1e-5, residual=res[lo:hi].clone(), quantize=quantize)
+        assert torch.equal(h[lo:hi].view(torch.int16), hs.view(torch.int16))
+        if quantize:
+            assert torch.equal(y.codes[lo:hi], ys.codes) and torch.equal(y.scale[lo:hi], ys.scale)
+        else:
+            assert torch.equal(y[lo:hi].view(torch.int16), ys.view(torch.int16))
+    assert torch.equal(h.view(torch.int16), (x.float() + res.float()).to(dt).view(torch.int16))
+    assert h_kept()
+
+
+@pytest.mark.parametrize("T,D,dtype", [(4099, 8192, "bf16"), (8197, 4104, "fp16"), (32771, 1024, "bf16"),
+                                       (4099, 8193, "bf16"), (2050, 16384, "bf16")])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_norm_backward_of_large_batches(T, D, dtype, in_place):
+    say(f"[norm backward, large] {T} x {D} {dtype} in_place={in_place}")
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    dy, h, add = (torch.randn((T, D), generator=g, device="cuda").to(dt) for _ in range(3))
+    w = torch.randn(D, generator=g, device="cuda")
+    dy0 = dy.clone()
+    got = api.rmsnorm_bwd(dy, h, w, 1e-5, dx_add=add, dx=dy if in_place else None)
+    for lo, hi in ((0, 9), (T // 2, T // 2 + 5), (T - 7, T)):
+        few = api.rmsnorm_bwd(dy0[lo:hi].clone(), h[lo:hi].clone(), w, 1e-5, dx_add=add[lo:hi].clone())
+        assert torch.equal(got.dx[lo:hi].view(torch.int16), few.dx.view(torch.int16))
+    ref, size = (torch.zeros(D, dtype=torch.float64, device="cuda") for _ in range(2))
+    for lo in range(0, T, 1024):
+        hd = h[lo:lo + 1024].double()
+        n = dy0[lo:lo + 1024].double() * hd * (hd.square().mean(1, keepdim=True) + 1e-5).rsqrt()
+        ref += n.sum(0)
+        size += n.abs().sum(0)
+    within(got.d_weight, f64(ref), U[torch.float32] * np.abs(f64(ref)) + 1e-5 * f64(size), "dw")
+
+
 def test_norm_gradient_against_differences():
     """The kernel's dx and dw against differences of the definition along random directions."""
     say("[norm bwd] differences")
