@@ -66,9 +66,8 @@ QL_DEV float inv_rms(float ss, int D, float eps, float pre) {
 
 }  // namespace
 
-// y = n w of a row per team.  2048 x 8192 with a residual: to 16 bits (134 MB) 25.9 us,
-// 5.2 TB/s; to 8 bits (117 MB) 24.2 us, the second reduction, of the maximum, standing
-// between the loads and the codes.  8192 x 1024 runs at 6.3 TB/s.
+// y = n w of a row per team.  2048 x 8192 with a residual: to 16 bits (134 MB) 25.4 us,
+// 5.3 TB/s; to 8 bits (117 MB) 20.2 us, 5.8 TB/s (26.1 with h stored through the caches).  8192 x 1024 runs at 6.3 TB/s.
 template <bool F16, bool Q8, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
     __shared__ float slots[2][32];
@@ -179,10 +178,10 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
 // held in registers, the next row's loads issued before this row's sums (kHold); longer
 // ones are read again after the sums, from the caches.
 //
-// 4096 x 8192 with dx_add and fp32 weights, 268 MB: 48.4 us, 5.5 TB/s, and 4.8 us for
-// the sum of the partials.  One workgroup a CU (256): with two 61.9 us in all, against
-// 55.7, with three 68.7 (more partials, and the held rows leave no registers for a second
-// one).
+// 4096 x 8192 with dx_add and fp32 weights, 268 MB: 46.6 us, 5.8 TB/s (FAR; 48.4 through the
+// caches), and 4.7 us for the sum of the partials.  One workgroup a CU (256): through the
+// caches with two 61.9 us in all, against 55.7, with three 68.7 (more partials, and the held
+// rows leave no registers for a second one).
 template <bool F16, bool DW, bool FAR, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, int64_t teams) {
     __shared__ float slots[2][32];
