@@ -174,7 +174,7 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
 
 // dx of a row per team and step, the teams striding over the rows.  A lane holds the
 // same columns of every row, so its share of dw stays in registers, and one fp32
-// partial row per workgroup is written at the end (DW).  Rows up to 8192 values are
+// partial row per workgroup is written at the end (DW).  Rows up to 12288 values are
 // held in registers, the next row's loads issued before this row's sums (kHold); longer
 // ones are read again after the sums, from the caches.
 //
@@ -378,6 +378,16 @@ void for_norm_team(int64_t D, Go go) {
 // In the backward a template argument: a branch around the loads cost 57 us against 49.6.
 constexpr int64_t kFarValues = int64_t(1) << 24;
 
+// The backward holds rows of up to 12288 values in 512 threads (us, 1024 threads that read
+// the row twice / 512 that hold it: 2048 x 11008 68.9 / 55.5, 4096 x 8448 133.8 / 98.4; with
+// four chunks a thread, 4096 x 16384, registers spill: 133.6 / 159.9).
+template <class Go>
+void for_bwd_team(int64_t D, Go go) {
+    const int64_t c = ceil_div(D, 8);
+    if (c > 1024 && c <= 1536) go(std::integral_constant<int, 512>{}, std::integral_constant<int, 3>{});
+    else for_norm_team(D, go);
+}
+
 // Workgroups of the backward (one a CU) and its teams
 constexpr int64_t kBwdGroups = 256;
 int64_t bwd_per(int64_t D) { return D <= 2048 ? 4 : 1; }
@@ -406,7 +416,7 @@ int64_t rmsnorm_bwd_partials(int64_t T, int64_t D) { return bwd_groups(T, D); }
 hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16) {
     const int64_t groups = bwd_groups(a.T, a.D), teams = groups * bwd_per(a.D);
     const bool far = a.T * a.D >= 2 * kFarValues && a.D % 8 == 0;
-    for_norm_team(a.D, [&](auto lanes, auto ch) {
+    for_bwd_team(a.D, [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
         const dim3 g((unsigned)groups), b(team_threads(L));
         const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, g, b, 0, s, a, teams); };
