@@ -50,7 +50,7 @@ int rows8_dequantize_f16(const int8_t* codes, const float* scale, int64_t R, int
  *     h = RNE_16(x + residual)             (x without a residual)
  *     y = h (mean(h^2) + eps)^(-1/2) w     (w = 1 without a weight)
  *   in fp32, the sum of squares over a whole row included (rows whose squares
- *   leave fp32 are summed scaled down), with one rounding at each output.  The
+ *   leave fp32 at either end are summed scaled), with one rounding at each output.  The
  *   norm is that of the 16-bit h, so that the backward below, which reads h,
  *   differentiates what was computed.  A row that holds an inf or NaN gives
  *   what the formula gives: NaN at an inf and 0 beside it, NaN in all of a row

@@ -55,13 +55,23 @@ QL_DEV void weight_values(const WChunk& k, bool wide, float (&v)[8]) {
     }
 }
 
-// Rows whose squares leave fp32 (rms above 2^64 / sqrt D) are summed scaled by this
-// power of two (exact); the sum of an inf stays inf (r = 0), of a NaN NaN.
-constexpr float kHuge = 0x1p-72f;
+// Rows whose squares leave fp32 are summed again scaled by a power of two (exact), eps with
+// its square:
+//   above (the sum and eps over 2^128): 2^-72; the sum of an inf stays inf (r = 0), of a NaN NaN;
+//   below (both under 2^-40): 2^64.  Squares of values below 2^-63 lose bits, and the
+//     hardware's rsq takes an argument below 2^-126 as 0, whose root would make a row of zeros
+//     0 * inf.  Scaled, eps alone is at least 2^-21.
+constexpr float kHuge = 0x1p-72f, kTiny = 0x1p64f;
 
-// 1 / sqrt of the mean square of the row times `pre` (1 or kHuge), eps scaled with it
+// the power of two for a row's unscaled sum of squares (the same in the whole team)
+QL_DEV float row_scale(float ss, float eps) {
+    const float both = ss + eps;
+    return !(both < __builtin_inff()) ? kHuge : both < 0x1p-40f ? kTiny : 1.0f;
+}
+
+// 1 / sqrt of the mean square of the row times `pre`, eps scaled with it
 QL_DEV float inv_rms(float ss, int D, float eps, float pre) {
-    return __builtin_amdgcn_rsqf(ss / (float)D + (pre == 1.0f ? eps : eps * (kHuge * kHuge)));
+    return __builtin_amdgcn_rsqf(ss / (float)D + eps * pre * pre);
 }
 
 }  // namespace
@@ -118,10 +128,9 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
         }
         return s;
     };
-    float pre = 1.0f;
     float ss = team_sum<LANES>(squares(1.0f), slots[0]);
-    if (!(ss < __builtin_inff())) {                     // the same in the whole team
-        pre = kHuge;
+    const float pre = row_scale(ss, a.eps);
+    if (pre != 1.0f) {
         if constexpr (LANES > 64) __syncthreads();      // slots[0] is read
         ss = team_sum<LANES>(squares(pre), slots[0]);
     }
@@ -258,11 +267,11 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
                 }
             }
         };
-        float pre = 1.0f, ss, gh;
+        float ss, gh;
         sums(1.0f, ss, gh);
         team_sum2<LANES>(ss, gh, slots[par]);
-        if (!(ss < __builtin_inff())) {
-            pre = kHuge;
+        const float pre = row_scale(ss, a.eps);
+        if (pre != 1.0f) {
             if constexpr (LANES > 64) __syncthreads();
             sums(pre, ss, gh);
             team_sum2<LANES>(ss, gh, slots[par]);
