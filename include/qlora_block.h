@@ -78,7 +78,8 @@ int rmsnorm_fwd_f16(const uint16_t* x, const uint16_t* residual, int64_t T, int6
  *   n = h r and g = dY w:
  *     dx = r (g - n mean(g n)) + dx_add
  *     dw = sum over rows of dY n
- *   in fp32, the same bits on every run.  dx is the gradient of x and of the
+ *   in fp32 (g, dx and dw have to lie in its range; the squares and g h need
+ *   not), the same bits on every run.  dx is the gradient of x and of the
  *   residual alike; dx_add is what reaches h on the residual path.
  *   dy, h     [T, D] 16-bit, read (h: the forward's, or its x without a residual).
  *   weight    as in the forward.

@@ -2,9 +2,10 @@
 // gfx950.  With r = (mean(h^2) + eps)^(-1/2), n = h r and g = dy w:
 //   y  = n w
 //   dx = r (g - n mean(g n)) + dx_add,   dw = sum over rows of dy n
-// (d r / d h_j = -r^3 h_j / D, so the norm's slope takes from g its part along
-// n).  Both are bound by HBM: a row stays in its team's registers (rows.hpp),
-// every input is read once and every output written once.
+// (d r / d h_j = -r^3 h_j / D, so the norm's slope takes from g its part along n;
+// mean(g n) is r mean(g h), so that one pass over a row gives both sums).  Both are
+// bound by HBM: a row stays in its team's registers (rows.hpp), every input is read
+// once and every output written once.
 #include <algorithm>
 
 #include "rows.hpp"
@@ -253,32 +254,57 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, 
                 weight_values<F16>(wc, wide, g);
             }
         };
-        const auto sums = [&](float pre, float& ss, float& gh) {
-            ss = gh = 0.0f;
-#pragma unroll
-            for (int j = 0; j < CH; ++j) {
+        // over the row's values: f(sum, h, dy w)
+        const auto sum = [&](auto f) {
+            float s = 0.0f;
+            const auto add = [&](int j) {
                 float h[8], dy[8], g[8];
                 chunk(j, h, dy, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = h[e] * pre;
-                    ss = fmaf(u, u, ss);
-                    gh = fmaf(dy[e] * g[e], u, gh);
-                }
+                for (int e = 0; e < 8; ++e) s = f(s, h[e], dy[e] * g[e]);
+            };
+            if constexpr (kHold) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) add(j);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < CH; ++j) add(j);
             }
+            return s;
         };
-        float ss, gh;
-        sums(1.0f, ss, gh);
+        float ss = 0.0f, gh = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            float h[8], dy[8], g[8];
+            chunk(j, h, dy, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(h[e], h[e], ss);
+                gh = fmaf(dy[e] * g[e], h[e], gh);
+            }
+        }
         team_sum2<LANES>(ss, gh, slots[par]);
         const float pre = row_scale(ss, a.eps);
-        if (pre != 1.0f) {
+        float r = inv_rms(ss, D, a.eps, 1.0f);
+        float m = gh * r * invD;                        // mean(g n)
+        // The squares or g h leave fp32: first r, then the mean from n itself.  The branch below
+        // costs least as an unlikely one where the row is held (2048 x 4096 19.2 -> 19.4 us for
+        // the whole case, 2048 x 11008 unchanged), and as a uniform one where it is read again
+        // (1000 x 20000 104 -> 98 us, as an unlikely one 112: the registers spill elsewhere).
+        const bool rare = pre != 1.0f || !(fabsf(m) < __builtin_inff());
+        const auto again = [&]() {
             if constexpr (LANES > 64) __syncthreads();
-            sums(pre, ss, gh);
-            team_sum2<LANES>(ss, gh, slots[par]);
+            ss = team_sum<LANES>(sum([&](float s, float h, float) { return fmaf(h * pre, h * pre, s); }), slots[par]);
+            r = inv_rms(ss, D, a.eps, pre);
+            if constexpr (LANES > 64) __syncthreads();
+            m = team_sum<LANES>(sum([&](float s, float h, float g) { return fmaf(g, h * pre * r * invD, s); }), slots[par]);
+        };
+        if constexpr (kHold) {
+            if (__builtin_expect(rare, 0)) again();
+        } else {
+            if (__builtin_amdgcn_readfirstlane(rare)) again();
         }
         par ^= 1;
-        const float r = inv_rms(ss, D, a.eps, pre);
-        const float m = gh * r * invD;                  // mean(g n)
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             // the packed values are what stays in registers over the sums, not their fp32 forms

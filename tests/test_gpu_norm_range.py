@@ -84,3 +84,26 @@ def test_eps_as_large_as_the_squares(D):
     within(g.dx, rdx, bwd_bound(rdx, f64(dy), f64(x), f64(w), float(np.float32(eps)), dt), "dx")
     terms = np.abs(f64(dy) * oracle.rmsnorm(f64(x), None, eps)).sum(0)
     within(g.d_weight, rdw, U[torch.float32] * np.abs(rdw) + 1e-5 * terms + TINY[torch.float32], "dw")
+
+
+@pytest.mark.parametrize("D", SIZES)
+@pytest.mark.parametrize("h_size,dy_size", [(2.0 ** 33, 2.0 ** 100), (2.0 ** 100, 2.0 ** 100), (1.0, 2.0 ** 120),
+                                            (2.0 ** 120, 2.0 ** 90)])
+@pytest.mark.parametrize("weight", [True, False])
+def test_gradients_whose_products_leave_fp32(D, h_size, dy_size, weight):
+    """dY h beyond 2^128 where dx and dw are ordinary numbers: mean(g n) is formed from n."""
+    say(f"[norm range] D={D} h about {h_size:g} dy about {dy_size:g} weight={weight}")
+    dt, n, T = torch.bfloat16, make(D), 5
+    h, dy = n(T, D, dt=torch.float32), n(T, D, dt=torch.float32)
+    h[1:4] *= h_size                                       # an ordinary row before and behind them
+    dy[1:4] *= dy_size
+    h, dy = h.to(dt), dy.to(dt)
+    w = (1 + 0.3 * n(D, dt=torch.float32)) if weight else None
+    g = api.rmsnorm_bwd(dy, h, w, 1e-6)
+    torch.cuda.synchronize()
+    e32, wv = float(np.float32(1e-6)), None if w is None else f64(w)
+    rdx, rdw = oracle.rmsnorm_bwd(f64(dy), f64(h), wv, 1e-6)
+    within(g.dx, rdx, bwd_bound(rdx, f64(dy), f64(h), wv, e32, dt), "dx")
+    if w is not None:
+        terms = np.abs(f64(dy) * oracle.rmsnorm(f64(h), None, 1e-6)).sum(0)
+        within(g.d_weight, rdw, U[torch.float32] * np.abs(rdw) + 1e-5 * terms + TINY[torch.float32], "dw")
