@@ -103,9 +103,10 @@ size_t rmsnorm_workspace_bytes_bwd(int64_t T, int64_t D);
  *   epilogue of qlora_linear_act_fwd.
  *     Z = (sum_k xq[t, k] wq[n, k]) dx[t] dw[n] + bias
  *     Y = act(Z) * mul + residual
- *   The sum is exact (int32); everything after it is fp32 with one rounding at
- *   Y, and the bits do not depend on how the work is split.  A NaN scale makes
- *   its row of Y (its column, for a channel of W) NaN.
+ *   The sum is exact (int32); everything after it is fp32, operation by
+ *   operation as written (the smaller scale first), with one rounding at Y: the
+ *   bits of an output depend neither on T and N nor on how the work is split.  A
+ *   NaN scale makes its row of Y (its column, for a channel of W) NaN.
  *   x_codes [T, QLORA_ROWS8_PITCH(K)], x_scale [T]; w_codes [N, same pitch],
  *   w_scale [N]: as rows8_quantize or rmsnorm_fwd writes them (zeros past K).
  *   T 1 .. QLORA_ROWS_MAX, N 1 .. 2^20, K 1 .. QLORA_ROWS8_MAX, T N and T K at most 2^30.

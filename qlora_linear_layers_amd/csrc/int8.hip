@@ -25,8 +25,12 @@ QL_DEV EpiOperands epi_load(const Int8Args& a, int64_t t, int64_t n) {
     return {a.xs[t], a.ws[n], *(a.ep.bias ? a.ep.bias + n : none), *(a.ep.mul ? a.ep.mul + at : none),
             *(a.ep.res ? a.ep.res + at : none)};
 }
+// The epilogue's steps are rounded one by one, here as in k_int8_tile and k_int8_fin:
+// contracted into fmas in some places and not in others, the bits of an output would
+// depend on the kernel that forms it and on N % 8.
 template <bool F16>
 QL_DEV uint16_t epi_value(const Int8Args& a, const EpiOperands& o, int sum) {
+#pragma clang fp contract(off)
     float z = int8_scaled(sum, o.xs, o.ws);
     if (a.ep.bias) z += value16<F16>(o.bias);
     z = act_of(a.ep.act, z);
@@ -238,6 +242,7 @@ constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }  
 constexpr int kActPart = -1;
 template <bool F16, int ACT, int BN, int BM, int WN, int WM, int S>
 QL_DEV void int8_tile(const Int8Args& a, lds8_t* const (&buf)[S]) {
+#pragma clang fp contract(off)
     using Tile = Int8Tile<BN, BM, WN, WM>;
     constexpr int NI = Tile::NI, NJ = Tile::NJ;
     const int gn = ((int)a.N + BN - 1) / BN, gt = ((int)a.T + BM - 1) / BM;
@@ -512,6 +517,7 @@ void launch_tiles(const Int8Args& a, hipStream_t s) {
 // eight go one by one.
 template <bool F16, int S>
 __global__ __launch_bounds__(64) void k_int8_fin(Int8Args a) {
+#pragma clang fp contract(off)
     const int N = (int)a.N, NP = (N + 7) & ~7;
     const int n = ((int)blockIdx.x * 64 + (int)threadIdx.x) * 8;
     const int64_t t = blockIdx.y;
