@@ -336,7 +336,8 @@ def product_bits(x8, w8, dt):
     return round16(((s * np.minimum(a, b)) * np.maximum(a, b)).astype(np.float64), dt).reshape(s.shape)
 
 
-# token counts around every kernel's tile edges; channels and lengths from one on, odd ones among them
+# token counts around the decode kernel's groups and the edges of 64- and 128-token tiles (products of more tiles:
+# test_gpu_block_routes.py); channels and lengths from one on, odd ones among them
 PRODUCTS = [(1, 1, 1), (1, 70, 5), (2, 64, 128), (3, 17, 64), (15, 100, 127), (16, 256, 129), (17, 33, 300), (32, 320, 256),
             (33, 130, 1000), (48, 1000, 512), (64, 64, 640), (65, 257, 384), (100, 512, 1024), (129, 300, 4099),
             (200, 1024, 2048), (256, 256, 256), (257, 511, 130), (300, 4097, 777), (513, 200, 1280), (777, 1024, 512),

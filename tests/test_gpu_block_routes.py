@@ -1,5 +1,5 @@
 """Every kernel of the 8-bit product, at sizes that leave remainders in each direction, with
-every epilogue.
+every epilogue; and the norm's backward where long rows are read past the caches.
 
 An 8-bit product without an activation (or with relu) is a fixed sequence of fp32 operations,
 
@@ -15,7 +15,7 @@ import torch
 import oracle
 from qlora_linear_layers_amd import api
 from helpers import say
-from test_gpu_block import DT, behind, make, rows8_of
+from test_gpu_block import DT, TINY, U, behind, f64, make, rows8_of, within
 
 # One row per kernel of the product, (T, N, K): the decode kernel with 16 and with 32 tokens a
 # workgroup; tiles of 64 and 128 tokens, whole and with their reduction split (2 to 8 times);
@@ -169,3 +169,50 @@ def test_every_kernel_gives_a_token_the_same_bits(route, T, N, K, act, dtype, bi
         assert same(part(rows, cols), y[rows]), (lo, hi)
     for cols in (slice(0, max(1, N // 2 - 3)), slice(N // 3, N), slice(N - 1, N)):
         assert same(part(slice(0, T), cols), y[:, cols].contiguous()), cols
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,K", [s for r in ("64 split", "128 split") for s in ROUTES[r]])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_epilogue_of_split_products(T, N, K, act, dtype):
+    """Against the oracle, with the bound of test_gpu_block.py."""
+    say(f"[int8 routes] epilogue of splits T={T} N={N} K={K} {act} {dtype}")
+    n, dt = make(T + N + K), DT[dtype]
+    x8, w8 = rows8_of(n, T, K), rows8_of(n, N, K, std=2 * K ** -0.5)
+    b, m, r = operands(T + N + K, T, N, dt)
+    y, y_ok = behind(T, N, dt)
+    api.int8_linear_fwd(x8, w8, bias=b, act=act, mul=m, residual=r, out=y)
+    torch.cuda.synchronize()
+    assert y_ok()
+    ry, rz = oracle.int8_linear(x8.codes.cpu().numpy(), f64(x8.scale), w8.codes.cpu().numpy(), f64(w8.scale), f64(b), act,
+                                f64(m), f64(r))
+    mag = np.abs(rz) + np.abs(oracle.act(rz, act)) + np.abs(f64(b))
+    within(y, ry, U[dt] * np.abs(ry) + 2e-5 * mag * np.abs(f64(m)) + 2.0 ** -23 * np.abs(f64(r)) + TINY[dt], "y")
+
+
+# Rows of 8193 .. 12288 values (512 threads of three chunks), read past the caches where a batch is large
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,dtype", [(4099, 8456, "bf16"), (3001, 12288, "fp16"), (4099, 8200, "fp16"),
+                                       (3600, 11008, "bf16"), (3001, 11999, "bf16")])
+@pytest.mark.parametrize("add", [True, False])
+def test_norm_backward_of_long_rows_in_large_batches(T, D, dtype, add):
+    say(f"[norm backward, large] {T} x {D} {dtype} add={add}")
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    dy, h, ad = (torch.randn((T, D), generator=g, device="cuda").to(dt) for _ in range(3))
+    w = torch.randn(D, generator=g, device="cuda")
+    cut = lambda lo, hi: ad[lo:hi].clone() if add else None
+    got = api.rmsnorm_bwd(dy, h, w, 1e-5, dx_add=ad if add else None)
+    frozen = api.rmsnorm_bwd(dy, h, w, 1e-5, dx_add=ad if add else None, weight_grad=False)
+    assert same(got.dx, frozen.dx)
+    for lo, hi in ((0, 9), (T // 2, T // 2 + 5), (T - 7, T)):
+        few = api.rmsnorm_bwd(dy[lo:hi].clone(), h[lo:hi].clone(), w, 1e-5, dx_add=cut(lo, hi))
+        assert same(got.dx[lo:hi], few.dx), (lo, hi)
+    ref, size = (torch.zeros(D, dtype=torch.float64, device="cuda") for _ in range(2))
+    for lo in range(0, T, 1024):
+        hd = h[lo:lo + 1024].double()
+        terms = dy[lo:lo + 1024].double() * hd * (hd.square().mean(1, keepdim=True) + 1e-5).rsqrt()
+        ref += terms.sum(0)
+        size += terms.abs().sum(0)
+    within(got.d_weight, f64(ref), U[torch.float32] * np.abs(f64(ref)) + 1e-5 * f64(size), "dw")
