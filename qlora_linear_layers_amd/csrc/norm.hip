@@ -402,16 +402,23 @@ void for_norm_team(int64_t D, Go go) {
     else go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
-// From here on h is stored past the caches (it is read again behind a block's products or
-// in the backward), and from twice as many values on the backward reads its rows, for the
-// last time, that way: what the next kernel needs stays in the 256 MB cache instead.  With
-// a consumer of y (dx) behind each call, us without / with: forward 2048 x 8192 35.4 / 32.0,
-// 4096 x 8192 66.4 / 62.1, backward 4096 x 8192 74.4 / 69.0, 8192 x 8192 154 / 126, 32768 x
-// 1024 70 / 67.  Below, everything fits the cache: forward 2048 x 4096 with h read next 17.2 /
-// 19.0, backward 2048 x 4096 25.0 / 26.5.  (Where h is read at once at 2048 x 8192, 30.8 / 33.4.)
-// Not for rows of odd alignment, whose lines are read twice: backward 777 x 4099 28.4 / 33.3.
-// In the backward a template argument: a branch around the loads cost 57 us against 49.6.
-constexpr int64_t kFarValues = int64_t(1) << 24;
+// What passes by the caches, so that what the next kernel needs stays in them.
+//
+// Forward: h, which a block reads again behind its products or in the backward, where it is
+// larger than the L2 caches of the eight XCDs together.  us with it stored through / past the
+// caches, with a consumer of y (16 bits) behind each call: 1722 x 8192 (27 MiB of h) 27.3 /
+// 26.9, 2048 x 8192 35.8 / 31.9, 4096 x 8192 67.1 / 62.5; 3444 x 4096 29.2 / 27.0, 4096 x 4096
+// 35.3 / 31.0; y in 8 bits 26.9 / 25.0, 31.3 / 28.7 and 59.2 / 56.2; odd rows gain alike (4000 x
+// 4099 46.0 / 40.0).  Where h is read at once instead, storing it past the caches costs: 1024 x
+// 8192 17.0 / 18.5, 2048 x 8192 34.6 / 35.9, 4096 x 8192 67.6 / 68.4.
+//
+// Backward: its rows, read for the last time, where the call touches more than the 256 MiB
+// cache behind them.  With dx_add (8 bytes a value) 3444 x 8192 (215 MiB) 44.5 / 44.0, 4096 x
+// 8192 51.5 / 49.3, 8192 x 8192 103 / 88; 27554 x 1024 40.2 / 41.0, 38967 x 1024 58.4 / 54.5.
+// Without (6 bytes) 4870 x 8192 (228 MiB) 46.9 / 47.0, 5792 x 8192 54.1 / 53.3, 8192 x 8192 80.8 /
+// 69.4.  Not for rows of odd alignment, whose lines are read twice: 8200 x 4099 174 / 198, 4100 x
+// 8194 97 / 102.  A template argument there: a branch around the loads cost 57 us against 49.6.
+constexpr int64_t kL2Bytes = int64_t(32) << 20, kCacheBytes = int64_t(256) << 20;
 
 // The backward holds rows of up to 12288 values in 512 threads (us, 1024 threads that read
 // the row twice / 512 that hold it: 2048 x 11008 68.9 / 55.5, 4096 x 8448 133.8 / 98.4; with
@@ -431,7 +438,7 @@ int64_t bwd_groups(int64_t T, int64_t D) { return std::min(kBwdGroups, ceil_div(
 }  // namespace
 
 hipError_t launch_rmsnorm(NormArgs a, hipStream_t s, bool f16) {
-    a.far = a.T * a.D >= kFarValues;
+    a.far = a.T * a.D * 2 >= kL2Bytes;
     for_norm_team(a.D, [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
         const dim3 g((unsigned)ceil_div(a.T, team_threads(L) / L)), b(team_threads(L));
@@ -450,7 +457,7 @@ int64_t rmsnorm_bwd_partials(int64_t T, int64_t D) { return bwd_groups(T, D); }
 
 hipError_t launch_rmsnorm_bwd(const NormBwd& a, hipStream_t s, bool f16) {
     const int64_t groups = bwd_groups(a.T, a.D), teams = groups * bwd_per(a.D);
-    const bool far = a.T * a.D >= 2 * kFarValues && a.D % 8 == 0;
+    const bool far = a.T * a.D * (a.add ? 8 : 6) >= kCacheBytes && a.D % 8 == 0;
     for_bwd_team(a.D, [&](auto lanes, auto ch) {
         constexpr int L = decltype(lanes)::value, C = decltype(ch)::value;
         const dim3 g((unsigned)groups), b(team_threads(L));

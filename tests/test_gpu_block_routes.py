@@ -191,10 +191,12 @@ def test_epilogue_of_split_products(T, N, K, act, dtype):
     within(y, ry, U[dt] * np.abs(ry) + 2e-5 * mag * np.abs(f64(m)) + 2.0 ** -23 * np.abs(f64(r)) + TINY[dt], "y")
 
 
-# Rows of 8193 .. 12288 values (512 threads of three chunks), read past the caches where a batch is large
+# Rows of 8193 .. 12288 values (512 threads of three chunks), and batches that pass by the caches with dx_add (256 MiB
+# at 8 bytes a value) and without (6 bytes)
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,D,dtype", [(4099, 8456, "bf16"), (3001, 12288, "fp16"), (4099, 8200, "fp16"),
-                                       (3600, 11008, "bf16"), (3001, 11999, "bf16")])
+                                       (3600, 11008, "bf16"), (3001, 11999, "bf16"), (5500, 8200, "bf16"),
+                                       (43711, 1032, "fp16"), (10950, 4088, "bf16")])
 @pytest.mark.parametrize("add", [True, False])
 def test_norm_backward_of_long_rows_in_large_batches(T, D, dtype, add):
     say(f"[norm backward, large] {T} x {D} {dtype} add={add}")
