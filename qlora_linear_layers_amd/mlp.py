@@ -99,7 +99,7 @@ class GatedMlp:
 @dataclass
 class NormMlpSaved:
     """What a training forward keeps for the backward."""
-    h: torch.Tensor      # the residual stream in front of the norm, 16 bits
+    h: torch.Tensor      # the residual stream in front of the norm, 16 bits (x itself where nothing was added to it)
     mlp: MlpSaved
 
     def nbytes(self):
@@ -160,7 +160,8 @@ class Int8Mlp:
 
     @classmethod
     def from_block(cls, block, dtype=torch.bfloat16):
-        """Of a NormMlp: every adapter merged into its weight (in `dtype`), the weight's rows quantized."""
+        """Of a NormMlp: every adapter merged into its weight (in the adapter's dtype; a weight without one is
+        taken in `dtype`), the weight's rows quantized."""
         rows = (api.rows8_quantize(api.qlora_merge_lora(*layer.args(), dtype=dtype))
                 for layer in (block.mlp.gate, block.mlp.up, block.mlp.down))
         return cls(*rows, block.norm_weight, block.eps, block.mlp.act)
