@@ -169,8 +169,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_int8_skinny(Int8Args a) {
 //   S = 4 (128 x 128 and 128 x 64 where they are at most one a CU): loads run three tiles
 //     ahead.  Two waves a SIMD, each with one half of every K tile, gained 3% there
 //     (1024 tokens of 4096 x 4096 20.9 -> 20.3 us) and lost as much in split products.
-// 2048 tokens through 8192 -> 22016 with silu and mul: 329 to 338 us, 2.2 POP/s, MFMA busy
-// 0.67 of the cycles, no bank conflicts; on zeros 319 us where values took 354, so a part
+// 2048 tokens through 8192 -> 22016 with silu and mul: 328 to 345 us by the card, 2.2 POP/s, MFMA busy
+// 0.66 of the cycles, no bank conflicts; on zeros 319 us where values took 354, so a part
 // of the rest is the card's power (an MFMA-only loop reaches 4.94 POP/s on zeros, 3.5 on
 // values).  128 x 128 tiles, one a CU: 0.34 to 0.42 us a K tile, 32 KB each out of L2.
 // LDS rows are 128 bytes with their 16-byte chunks XOR-swizzled (lds_off); a direct load
@@ -600,7 +600,9 @@ struct Int8Plan {
         }
         route = T <= 64 ? Int8Route::Tile64 : Int8Route::Tile128;
         // Splits: rounds of K tiles at 0.34 us, and for the int32 sums, written and read
-        // back, 0.4 us a MB and 1.5 us of a launch.  Against 0.25 us a MB and 2 of a launch,
+        // back, 0.4 us a MB and 1.5 us of a launch (the time of a K tile is that of operands in
+        // the caches: 512 tokens through a cold 11008 -> 4096, 43 K tiles a workgroup, take 27 to
+        // 33 us).  Against 0.25 us a MB and 2 of a launch,
         // us: 128 tokens through 11008 -> 4096 18.9 / 20.2 (6 / 8 splits), 256 through 4096 ->
         // 1024 11.7 / 13.2; with 2.5 of a launch 256 through 4096 -> 4096 stay unsplit, 16.8
         // against 15.3, 300 through 5120 -> 5120 21.7 against 20.0.

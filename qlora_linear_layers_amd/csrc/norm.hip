@@ -5,7 +5,8 @@
 // (d r / d h_j = -r^3 h_j / D, so the norm's slope takes from g its part along n;
 // mean(g n) is r mean(g h), so that one pass over a row gives both sums).  Both are
 // bound by HBM: a row stays in its team's registers (rows.hpp), every input is read
-// once and every output written once.
+// once and every output written once; only the backward of rows past 12288 values
+// reads them twice.
 #include <algorithm>
 
 #include "rows.hpp"
@@ -77,8 +78,10 @@ QL_DEV float inv_rms(float ss, int D, float eps, float pre) {
 
 }  // namespace
 
-// y = n w of a row per team.  2048 x 8192 with a residual: to 16 bits (134 MB) 25.4 us,
-// 5.3 TB/s; to 8 bits (117 MB) 20.2 us, 5.8 TB/s (26.1 with h stored through the caches).  8192 x 1024 runs at 6.3 TB/s.
+// y = n w of a row per team.  With a residual, calls in a row over eight sets of inputs (more
+// than the caches hold): 2048 x 8192 to 16 bits (134 MB) 23.8 us, 5.6 TB/s, to 8 bits (117 MB)
+// 23.5, 2048 x 4096 13.4 and 13.2, 8192 x 1024 13.0.  Over three sets, which the last cache
+// mostly holds, 2048 x 8192 takes 19.9 and 19.8 (21.0 with h stored through the caches).
 template <bool F16, bool Q8, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
     __shared__ float slots[2][32];
@@ -186,12 +189,15 @@ __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm(NormArgs a) {
 // same columns of every row, so its share of dw stays in registers, and one fp32
 // partial row per workgroup is written at the end (DW).  Rows up to 12288 values are
 // held in registers, the next row's loads issued before this row's sums (kHold); longer
-// ones are read again after the sums, from the caches.
+// ones are read again after the sums, from the caches.  With dw, three chunks a thread of
+// held rows spill 60 to 72 bytes a lane at 256 registers, four chunks of 1024 threads 260 to
+// 320 at 128.
 //
 // 4096 x 8192 with dx_add and fp32 weights, 268 MB: 46.6 us, 5.8 TB/s (FAR; 48.4 through the
 // caches), and 4.7 us for the sum of the partials.  One workgroup a CU (256): through the
 // caches with two 61.9 us in all, against 55.7, with three 68.7 (more partials, and the held
-// rows leave no registers for a second one).
+// rows leave no registers for a second one).  Up to 6144 values, where 256 threads hold a row,
+// that is one wave a SIMD: 2048 x 4096 with dx_add 20.7 us in all against 11.3 for its 67 MB.
 template <bool F16, bool DW, bool FAR, int LANES, int CH>
 __global__ __launch_bounds__(team_threads(LANES)) void k_rmsnorm_bwd(NormBwd a, int64_t teams) {
     __shared__ float slots[2][32];
@@ -421,8 +427,8 @@ void for_norm_team(int64_t D, Go go) {
 constexpr int64_t kL2Bytes = int64_t(32) << 20, kCacheBytes = int64_t(256) << 20;
 
 // The backward holds rows of up to 12288 values in 512 threads (us, 1024 threads that read
-// the row twice / 512 that hold it: 2048 x 11008 68.9 / 55.5, 4096 x 8448 133.8 / 98.4; with
-// four chunks a thread, 4096 x 16384, registers spill: 133.6 / 159.9).
+// the row twice / 512 that hold it: 2048 x 11008 68.9 / 55.5, 4096 x 8448 with a consumer of dx
+// 133.8 / 98.4; with four chunks a thread, 4096 x 16384, more registers spill: 133.6 / 159.9).
 template <class Go>
 void for_bwd_team(int64_t D, Go go) {
     const int64_t c = ceil_div(D, 8);
